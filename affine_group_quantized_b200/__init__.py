@@ -39,6 +39,14 @@ class QmvError(RuntimeError):
         super().__init__(f"{func}: {_STATUS_NAMES.get(status, status)}: {message}")
 
 
+class _KVCacheStruct(ctypes.Structure):
+    """qmv_kv_cache of include/qmv.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "k_biases", "v_scales",
+                                                "v_biases")]
+                + [(n, ctypes.c_int) for n in ("num_pages", "num_kv_heads", "page_size",
+                                               "head_dim", "bits", "group_size")])
+
+
 _lib = None
 
 
@@ -76,13 +84,25 @@ def lib() -> ctypes.CDLL:
         L.affine_dequantize.restype = I
         L.qmv_quant_last_error.restype = ctypes.c_char_p
         L.qmv_quant_last_error.argtypes = []
+        Q, C = ctypes.c_longlong, ctypes.POINTER(_KVCacheStruct)
+        L.kv_append.argtypes = [C, P, P, Q, Q, P, P, P, I, I, I, P, P, P, I, P, P]
+        L.kv_read.argtypes = [C, P, P, Q, Q, P, P, P, I, I, I, P, P]
+        L.kv_attention.argtypes = [C, P, Q, P, P, P, I, I, I, ctypes.c_float, P, I, P,
+                                   ctypes.c_size_t, P, P]
+        L.kv_attention_workspace.argtypes = [C, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+        L.kv_evict.argtypes = [C] + [P] * 8 + [I] * 6 + [P, P]
+        for f in (L.kv_append, L.kv_read, L.kv_attention, L.kv_attention_workspace, L.kv_evict):
+            f.restype = I
+        L.qmv_kv_last_error.restype = ctypes.c_char_p
+        L.qmv_kv_last_error.argtypes = []
         _lib = L
     return _lib
 
 
 EXPORTED = ("qmv", "qmv_noalloc", "qvm", "qmv_trellis", "qmv_gate_up", "qmv_silu_gate_resid", "gather_qmv",
             "qmv_last_error", "qmv_abi_version", "qmv_device_status", "affine_quantize",
-            "affine_dequantize", "qmv_quant_last_error")
+            "affine_dequantize", "qmv_quant_last_error", "kv_append", "kv_read", "kv_attention",
+            "kv_attention_workspace", "kv_evict", "qmv_kv_last_error")
 
 
 def _ptr(a):
@@ -236,3 +256,185 @@ def affine_dequantize(w_q, scales, biases, w_hat, N, K, bits, group_size,
     _check_quant("affine_dequantize", lib().affine_dequantize(
         _ptr(w_q), _ptr(scales), _ptr(biases), _ptr(w_hat), N, K, bits,
         group_size, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache
+# ---------------------------------------------------------------------------
+
+
+def _check_kv(func: str, rc: int):
+    if rc != QMV_OK:
+        raise QmvError(func, rc, lib().qmv_kv_last_error().decode())
+
+
+class KVCache:
+    """A paged key-value cache: the buffers and shape that every ``kv_*`` call
+    takes (``qmv_kv_cache`` of include/qmv.h).  Rows (page, kv head, slot) of
+    ``head_dim`` elements, packed codes with bf16 scales and biases for
+    ``bits`` 4 or 8, bf16 rows (no scales; ``group_size`` ignored) for 16.
+    The object keeps the buffers alive and holds nothing else.
+    """
+
+    def __init__(self, k, v, k_scales, k_biases, v_scales, v_biases, num_pages, num_kv_heads,
+                 page_size, head_dim, bits, group_size):
+        rows = num_pages * num_kv_heads * page_size
+        for name, t in (("k", k), ("v", v)):
+            _need(name, t, rows * head_dim * bits // 8)
+        if bits != 16:
+            for name, t in (("k_scales", k_scales), ("k_biases", k_biases),
+                            ("v_scales", v_scales), ("v_biases", v_biases)):
+                _need(name, t, 2 * rows * (head_dim // max(group_size, 1)))
+        self.buffers = (k, v, k_scales, k_biases, v_scales, v_biases)
+        self.num_pages, self.num_kv_heads, self.page_size = num_pages, num_kv_heads, page_size
+        self.head_dim, self.bits, self.group_size = head_dim, bits, group_size
+        self._struct = _KVCacheStruct(*(_ptr(t) for t in self.buffers), num_pages, num_kv_heads,
+                                      page_size, head_dim, bits, group_size)
+        self._ref = ctypes.byref(self._struct)
+        self._device = _device_of(k)
+
+
+def _device_of(t):
+    """A tensor's CUDA device, or None for a plain address."""
+    if t is None or isinstance(t, int):
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    return t.device.index
+
+
+def _same_device(cache, **tensors):
+    """Every tensor, and the current device, must be the cache's: a launch
+    goes to the current device."""
+    import torch
+    want = cache._device
+    if want is None:
+        return
+    if torch.cuda.current_device() != want:
+        raise ValueError(f"the cache is on device {want}, the current device is "
+                         f"{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and not isinstance(t, int) and t.get_device() != want:
+            raise ValueError(f"{name}: not on the cache's device {want}")
+
+
+def _token_stride(name, t, stride, rows, heads, dim):
+    """The stride (elements) between the rows of a bf16 [rows, heads, dim]
+    argument, whose heads lie behind one another: a tensor's own, or the one
+    given (heads * dim when none is)."""
+    packed = heads * dim
+    if t is None or isinstance(t, int):
+        return packed if stride is None else stride
+    if stride is None and t.dim() == 3 and tuple(t.shape) == (rows, heads, dim):
+        if t.element_size() != 2:
+            raise ValueError(f"{name}: must hold bf16 values")
+        s0, s1, s2 = t.stride()
+        if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
+            raise ValueError(f"{name}: a row's heads must be contiguous")
+        return s0 if rows > 1 else packed
+    stride = packed if stride is None else stride
+    _need(name, t, 2 * ((rows - 1) * stride + packed) if rows > 0 else 0)
+    return stride
+
+
+def _need_int32(name, t, count):
+    if t is None or isinstance(t, int):
+        return
+    _need(name, t, 4 * count)
+    if t.element_size() != 4:
+        raise ValueError(f"{name}: must hold 4-byte values")
+
+
+def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
+              seen=None, positions=None, weights=None, state_width=0, k_stride=None,
+              v_stride=None, d_status=None, stream=None):
+    """Write num_tokens new tokens' keys and values into the cache: sequence b's
+    tokens token_starts[b] .. token_starts[b+1]-1 (one token each without
+    token_starts) fill its slots from lens[b] on (see include/qmv.h)."""
+    H, D = cache.num_kv_heads, cache.head_dim
+    ks = _token_stride("k", k, k_stride, num_tokens, H, D)
+    vs = _token_stride("v", v, v_stride, num_tokens, H, D)
+    _kv_rows_need(block_table, lens, token_starts, batch, table_width)
+    _need_int32("seen", seen, batch)
+    _need_int32("positions", positions, batch * H * state_width)
+    _need_int32("weights", weights, batch * H * state_width)
+    _same_device(cache, k=k, v=v, block_table=block_table, lens=lens, token_starts=token_starts,
+                 seen=seen, positions=positions, weights=weights, d_status=d_status)
+    _check_kv("kv_append", lib().kv_append(
+        cache._ref, _ptr(k), _ptr(v), ks, vs, _ptr(block_table), _ptr(lens), _ptr(token_starts),
+        batch, num_tokens, table_width, _ptr(seen), _ptr(positions), _ptr(weights), state_width,
+        _ptr(d_status), _stream(stream)))
+
+
+def _kv_rows_need(block_table, lens, token_starts, batch, table_width):
+    _need_int32("block_table", block_table, batch * table_width)
+    _need_int32("lens", lens, batch)
+    _need_int32("token_starts", token_starts, batch + 1)
+
+
+def kv_read(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
+            k_stride=None, v_stride=None, d_status=None, stream=None):
+    """Slots lens[b] .. of sequence b as dense bf16 rows token_starts[b] ..
+    token_starts[b+1]-1 of k and v: the reverse of kv_append."""
+    H, D = cache.num_kv_heads, cache.head_dim
+    ks = _token_stride("k", k, k_stride, num_tokens, H, D)
+    vs = _token_stride("v", v, v_stride, num_tokens, H, D)
+    _kv_rows_need(block_table, lens, token_starts, batch, table_width)
+    _same_device(cache, k=k, v=v, block_table=block_table, lens=lens, token_starts=token_starts,
+                 d_status=d_status)
+    _check_kv("kv_read", lib().kv_read(
+        cache._ref, _ptr(k), _ptr(v), ks, vs, _ptr(block_table), _ptr(lens), _ptr(token_starts),
+        batch, num_tokens, table_width, _ptr(d_status), _stream(stream)))
+
+
+def kv_attention_workspace(cache, batch, num_q_heads, table_width, with_weights=False) -> int:
+    """Bytes of workspace kv_attention needs for these sizes, whatever the lengths."""
+    n = ctypes.c_size_t(0)
+    _check_kv("kv_attention_workspace", lib().kv_attention_workspace(
+        cache._ref, batch, num_q_heads, table_width, 1 if with_weights else 0, ctypes.byref(n)))
+    return n.value
+
+
+def kv_attention(cache, q, block_table, lens, out, batch, num_q_heads, table_width, scale,
+                 workspace, weights=None, state_width=0, q_stride=None, d_status=None,
+                 stream=None):
+    """Attention of one new token per sequence over its lens[b] slots; with
+    weights, each slot's probabilities are added to them (see include/qmv.h).
+    workspace: a tensor of kv_attention_workspace's bytes."""
+    D = cache.head_dim
+    qs = _token_stride("q", q, q_stride, batch, num_q_heads, D)
+    _need("out", out, 2 * batch * num_q_heads * D)
+    _need_int32("block_table", block_table, batch * table_width)
+    _need_int32("lens", lens, batch)
+    _need_int32("weights", weights, batch * cache.num_kv_heads * state_width)
+    _need("workspace", workspace, 0)
+    if workspace is None or isinstance(workspace, int):
+        raise ValueError("workspace: must be a tensor")
+    _same_device(cache, q=q, block_table=block_table, lens=lens, out=out, weights=weights,
+                 workspace=workspace, d_status=d_status)
+    _check_kv("kv_attention", lib().kv_attention(
+        cache._ref, _ptr(q), qs, _ptr(block_table), _ptr(lens), _ptr(out), batch, num_q_heads,
+        table_width, scale, _ptr(weights), state_width, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(d_status), _stream(stream)))
+
+
+def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_weights,
+             new_positions, batch, table_width, state_width, budget, recent=0, sinks=0,
+             d_status=None, stream=None):
+    """Keep the `budget` slots of every (sequence, kv head) with the largest
+    weights, the newest `recent` and first `sinks` positions before all
+    others, and move them below budget (see include/qmv.h)."""
+    state = batch * cache.num_kv_heads * state_width
+    for name, t, n in (("block_table", block_table, batch * table_width), ("lens", lens, batch),
+                       ("seen", seen, batch), ("weights", weights, state),
+                       ("positions", positions, state), ("new_lens", new_lens, batch),
+                       ("new_weights", new_weights, state),
+                       ("new_positions", new_positions, state)):
+        _need_int32(name, t, n)
+    _same_device(cache, block_table=block_table, lens=lens, seen=seen, weights=weights,
+                 positions=positions, new_lens=new_lens, new_weights=new_weights,
+                 new_positions=new_positions, d_status=d_status)
+    _check_kv("kv_evict", lib().kv_evict(
+        cache._ref, _ptr(block_table), _ptr(lens), _ptr(seen), _ptr(weights), _ptr(positions),
+        _ptr(new_lens), _ptr(new_weights), _ptr(new_positions), batch, table_width, state_width,
+        budget, recent, sinks, _ptr(d_status), _stream(stream)))

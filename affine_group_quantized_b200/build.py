@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqmv.so")
-SOURCES = ["qmv_api.cu", "qmv_quant.cu", "qmv_qmm.cu"]
+SOURCES = ["qmv_api.cu", "qmv_quant.cu", "qmv_qmm.cu", "qmv_kv.cu", "qmv_kv_attn.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

@@ -49,6 +49,7 @@
 #ifndef LIBQMV_QMV_H
 #define LIBQMV_QMV_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -276,6 +277,137 @@ int affine_quantize(const void *w, uint32_t *w_q, void *scales, void *biases,
 int affine_dequantize(const uint32_t *w_q, const void *scales,
                       const void *biases, void *w_hat, int N, int K, int bits,
                       int group_size, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged key-value cache in the same format, and what writes and reads it
+ * ---------------------------------------------------------------------------
+ * The keys and the values of a cache are two affine matrices of the format
+ * above: row (page, kv head, slot) holds the head_dim elements of one token's
+ * head, so that affine_dequantize over all rows expands a whole cache.
+ *   k, v       bits 4 or 8: uint32 [num_pages, num_kv_heads, page_size,
+ *              head_dim*bits/32]; bits 16: bf16 rows of head_dim, as they are
+ *   *_scales, *_biases  bf16 [num_pages, num_kv_heads, page_size,
+ *              head_dim/group_size]; NULL (and group_size ignored) for bits 16
+ * A sequence's pages are named by its row of a block table, int32
+ * [batch, table_width] in device memory: slot j of sequence b lies in page
+ * block_table[b][j / page_size] at place j % page_size, and the sequence has
+ * table_width * page_size slots of room.  Entries past a sequence's last used
+ * slot are never read.  Lengths and the table stay on the device, so a
+ * captured call sees what they hold when it is replayed.
+ * Supported: bits in {4,8,16}; head_dim in {64,96,128,256}; group_size in
+ * {32,64,128} dividing head_dim; page_size a multiple of 16; fewer than 2^31
+ * rows (num_pages * num_kv_heads * page_size); batch <= 4096.
+ * Indices that the host cannot see are checked on the device: a page outside
+ * [0, num_pages), or a slot past the sequence's room, ORs 1 into *d_status
+ * (a device int or NULL, zeroed by the caller) and is neither read nor
+ * written.  On error qmv_kv_last_error() describes the failure.
+ */
+typedef struct {
+    void *k, *v;
+    void *k_scales, *k_biases, *v_scales, *v_biases;
+    int num_pages, num_kv_heads, page_size, head_dim, bits, group_size;
+} qmv_kv_cache;
+
+/*
+ * kv_append -- write new tokens' keys and values into the cache
+ *   k, v         bf16: token t's heads at k + t*k_stride (elements, a multiple
+ *                of 8, >= num_kv_heads*head_dim), [num_kv_heads, head_dim]
+ *                each (slices of one projection's output will do)
+ *   lens         int32 [batch]: slots already in use; a negative length marks
+ *                a row of the batch that is not in use (its tokens are skipped)
+ *   token_starts int32 [batch+1], non-decreasing: tokens token_starts[b] ..
+ *                token_starts[b+1]-1 belong to sequence b and fill its slots
+ *                from lens[b] on; NULL: one token per sequence
+ *                (num_tokens == batch).  Tokens outside every range (padding
+ *                behind the last sequence) are skipped.
+ *   seen, positions, weights: all NULL, or the slots' state for kv_evict,
+ *                int32 [batch], int32 and float [batch, num_kv_heads,
+ *                state_width], state_width >= table_width*page_size: the i-th
+ *                new token of sequence b gets position seen[b] + i and
+ *                accumulated weight 0
+ * Quantized rows are bit-identical to affine_quantize's.  lens is read, not
+ * advanced.  The pages written must not be shared by two tokens of the call.
+ * num_tokens = 0 enqueues nothing.  One kernel; no allocation.
+ */
+int kv_append(const qmv_kv_cache *cache, const void *k, const void *v, long long k_stride,
+              long long v_stride, const int *block_table, const int *lens,
+              const int *token_starts, int batch, int num_tokens, int table_width,
+              const int *seen, int *positions, float *weights, int state_width, int *d_status,
+              void *stream);
+
+/*
+ * kv_read -- rows of the cache as dense bf16, the reverse of kv_append
+ * The arguments of kv_append: slots lens[b] .. of sequence b are written to
+ * rows token_starts[b] .. token_starts[b+1]-1 of k and v, each value
+ * bf16(scale*q + bias) rounded once (affine_dequantize's), bf16 rows as they
+ * are.  Rows that belong to no sequence are left as they were.
+ */
+int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, long long v_stride,
+            const int *block_table, const int *lens, const int *token_starts, int batch,
+            int num_tokens, int table_width, int *d_status, void *stream);
+
+/*
+ * kv_attention -- attention of one new token per sequence over its cache
+ *   q        bf16: sequence b's heads at q + b*q_stride (elements, a multiple
+ *            of 8), [num_q_heads, head_dim]; num_q_heads a multiple of
+ *            num_kv_heads, head h reads kv head h / (num_q_heads/num_kv_heads)
+ *   lens     int32 [batch]: slots attended to, the new token's own among them
+ *   out      bf16 [batch, num_q_heads, head_dim]
+ *            s_hj = scale * sum_d q_hd K_jd,  p_h = softmax over j < lens[b],
+ *            out_h = sum_j p_hj V_j;  zeros where lens[b] <= 0
+ *   weights  NULL, or float [batch, num_kv_heads, state_width], state_width >=
+ *            table_width*page_size: weights[b][g][j] += sum of p_hj over the
+ *            heads h that read kv head g, for j < lens[b]
+ *   workspace  device memory of kv_attention_workspace's bytes, 16-byte
+ *            aligned; no contents are expected or kept.  Calls that may run at
+ *            the same time need workspaces of their own.
+ * Scores, softmax statistics and sums are fp32; a length past the sequence's
+ * room is cut to it and flagged, and slots of a page outside the cache take
+ * no part.  Results do not depend on timing (partial sums are joined in a
+ * fixed order).  batch = 0 enqueues nothing.  No allocation.
+ */
+int kv_attention(const qmv_kv_cache *cache, const void *q, long long q_stride,
+                 const int *block_table, const int *lens, void *out, int batch, int num_q_heads,
+                 int table_width, float scale, float *weights, int state_width, void *workspace,
+                 size_t workspace_bytes, int *d_status, void *stream);
+
+/* Bytes of workspace that kv_attention needs for these sizes, whatever the
+ * lengths, on the current device. */
+int kv_attention_workspace(const qmv_kv_cache *cache, int batch, int num_q_heads,
+                           int table_width, int with_weights, size_t *bytes);
+
+/*
+ * kv_evict -- keep the `budget` slots of each (sequence, kv head) that have
+ * gathered most attention weight
+ *   weights, positions  float and int32 [batch, num_kv_heads, state_width],
+ *            state_width >= table_width*page_size, as kv_append and
+ *            kv_attention keep them
+ *   seen     int32 [batch]: tokens the sequence has seen; slots whose position
+ *            is below `sinks`, or at least seen[b] - recent, are kept before
+ *            all others (recent + sinks <= budget)
+ * With n = lens[b]: if n > budget, the kept slots are the budget first in
+ * order: protected ones, the lower slot first, then the others by weight, the
+ * larger first, equal ones by the lower slot, NaN below every number.  Kept
+ * slots below budget stay where they are, and the i-th kept slot at or above budget
+ * moves into the i-th evicted slot below it: its key and value rows in place
+ * in the cache, its weight and position into new_weights and new_positions.
+ *   new_lens  int32 [batch]: min(n, budget) (0 for a negative length)
+ *   new_weights, new_positions  as weights and positions, and possibly the
+ *            same buffers: slots below new_lens[b] as they now are, slots from
+ *            there to n cleared (0 and -1), slots from n on left as they were
+ * A sequence's pages must be its own (no page in two rows of the table).
+ * Slots of a page outside the cache move only their state.  A length past the
+ * room is cut to it and flagged.  Room of at most 196608 slots.  batch = 0
+ * enqueues nothing.  One kernel; no allocation.
+ */
+int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens, const int *seen,
+             const float *weights, const int *positions, int *new_lens, float *new_weights,
+             int *new_positions, int batch, int table_width, int state_width, int budget,
+             int recent, int sinks, int *d_status, void *stream);
+
+/* Message for the last non-OK return of the kv_* entry points on this thread
+ * ("" if none). */
+const char *qmv_kv_last_error(void);
 
 /* Message for the last non-OK return of affine_quantize or
  * affine_dequantize on this thread ("" if none). */
