@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqmv.so")
-SOURCES = ["qmv_api.cu", "qmv_quant.cu", "qmv_qmm.cu", "qmv_kv.cu", "qmv_kv_attn.cu"]
+SOURCES = ["qmv_api.cu", "qmv_quant.cu", "qmv_qmm.cu", "qmv_kv.cu", "qmv_kv_attn4.cu",
+           "qmv_kv_attn8.cu", "qmv_kv_attn16.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

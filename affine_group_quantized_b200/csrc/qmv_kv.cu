@@ -2,7 +2,7 @@
 // kv_append (bf16 rows in, quantized or as they are), kv_read (dense bf16
 // rows out), kv_evict (the slots with the least accumulated attention weight
 // make room), and the C entry points, kv_attention's among them (its kernels
-// are in qmv_kv_attn.cu).  Contracts are in include/qmv.h.
+// are in qmv_kv_attn.cuh).  Contracts are in include/qmv.h.
 //
 // Append and read are streaming and element-wise: bf16 rows on one side, code
 // rows, scales and biases on the other.  A warp takes 32 chunks of 8 elements
@@ -780,7 +780,17 @@ static int check_attention(const char *f, const qmv_kv_cache *cache, const int *
                  num_q_heads, c->H);
   if (num_q_heads > 65535)
     return kfail(QMV_ERR_UNSUPPORTED, "%s: num_q_heads=%d above 65535", f, num_q_heads);
+  // tiles of 16 slots and (for the weights) score rows are numbered in 31 bits
+  if (static_cast<double>(batch) * num_q_heads * (static_cast<double>(width) * c->S / 16 + 1) >= 2147483648.0)
+    return kfail(QMV_ERR_UNSUPPORTED, "%s: batch * num_q_heads * room above 2^35", f);
   return QMV_OK;
+}
+
+static size_t attention_workspace(const qmvc::CacheView &c, int batch, int num_q_heads, bool weights,
+                                  int sms) {
+  return c.bits == 4   ? qmvc::attn_workspace_4(c, batch, num_q_heads, weights, sms)
+         : c.bits == 8 ? qmvc::attn_workspace_8(c, batch, num_q_heads, weights, sms)
+                       : qmvc::attn_workspace_16(c, batch, num_q_heads, weights, sms);
 }
 
 int kv_attention_workspace(const qmv_kv_cache *cache, int batch, int num_q_heads, int table_width,
@@ -793,7 +803,7 @@ int kv_attention_workspace(const qmv_kv_cache *cache, int batch, int num_q_heads
   if (rc) return rc;
   Device dev;
   if ((rc = current_device(f, &dev))) return rc;
-  *bytes = qmvc::attn_workspace(c, batch, num_q_heads, with_weights != 0, dev.sms);
+  *bytes = attention_workspace(c, batch, num_q_heads, with_weights != 0, dev.sms);
   return kok();
 }
 
@@ -817,7 +827,7 @@ int kv_attention(const qmv_kv_cache *cache, const void *q, long long q_stride,
   if (batch == 0) return kok();
   Device dev;
   if ((rc = current_device(f, &dev))) return rc;
-  const size_t need = qmvc::attn_workspace(a.cache, batch, num_q_heads, weights != nullptr, dev.sms);
+  const size_t need = attention_workspace(a.cache, batch, num_q_heads, weights != nullptr, dev.sms);
   if (need && !workspace) return kfail(QMV_ERR_NULL, "%s: workspace must not be NULL", f);
   if (workspace_bytes < need)
     return kfail(QMV_ERR_SHAPE, "%s: workspace of %zu bytes, the call needs %zu", f, workspace_bytes,
@@ -834,7 +844,9 @@ int kv_attention(const qmv_kv_cache *cache, const void *q, long long q_stride,
   a.state_width = state_width;
   a.workspace = workspace;
   a.stream = static_cast<cudaStream_t>(stream);
-  return launched(f, qmvc::attn_launch(a, dev.sms));
+  return launched(f, a.cache.bits == 4   ? qmvc::attn_launch_4(a, dev.sms)
+                     : a.cache.bits == 8 ? qmvc::attn_launch_8(a, dev.sms)
+                                         : qmvc::attn_launch_16(a, dev.sms));
 }
 
 int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens, const int *seen,

@@ -1,6 +1,6 @@
 // qmv_kv.h -- what the key-value cache sources share: the device view of a
 // paged cache, and the host interface of the attention kernels
-// (qmv_kv_attn.cu), used by the entry points in qmv_kv.cu.  Internal to the
+// (qmv_kv_attn.cuh), used by the entry points in qmv_kv.cu.  Internal to the
 // library.
 #pragma once
 
@@ -61,9 +61,14 @@ struct AttnArgs {
   cudaStream_t stream;
 };
 
-// Bytes of workspace a call needs; the launch itself (0 or a cudaError_t).
-size_t attn_workspace(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
-cudaError_t attn_launch(const AttnArgs &a, int sms);
+// Bytes of workspace a call needs, and the launches themselves, by width
+// (qmv_kv_attn4.cu, 8 and 16).
+size_t attn_workspace_4(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
+size_t attn_workspace_8(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
+size_t attn_workspace_16(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
+cudaError_t attn_launch_4(const AttnArgs &a, int sms);
+cudaError_t attn_launch_8(const AttnArgs &a, int sms);
+cudaError_t attn_launch_16(const AttnArgs &a, int sms);
 
 // A launch that may be scheduled while the previous kernel of the stream
 // finishes: the kernels hold their first global access until then

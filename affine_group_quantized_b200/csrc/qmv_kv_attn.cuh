@@ -1,0 +1,1230 @@
+// qmv_kv_attn.cuh -- attention of one new token per sequence over the paged
+// cache: the kernel behind kv_attention.  Each of qmv_kv_attn4.cu, 8 and 16
+// instantiates it for one width.
+//
+// The mathematics.  Codes are multiplied as the integers they are, and scales
+// and biases applied outside the products: with groups g of a row,
+//   s_j   = f * sum_g (sk_jg * sum_{d in g} x_d q_jd + bk_jg * sum_{d in g} x_d)
+//   out_d = (sum_j (p_j sv_jg) q_jd + sum_j p_j bv_jg) / sum_j p_j
+// so a score costs two fp32 multiply-adds per group beyond its matrix product,
+// and the values one multiplication of the probability per group.  Scores are
+// kept in units of log2, p_j = 2^(s_j - m), with a running maximum m that is
+// raised (and the sums rescaled) only when a score exceeds it by 3, so p <= 8.
+//
+// Matrix products.  A step takes 16 slots.  Scores: A = 16 slots x 16 elements
+// of codes, B = 16 elements x 8 query heads, C = slots x heads.  Values: A = 16
+// elements x 16 slots, B = slots x heads (the probabilities, transposed 8x8 in
+// registers by movmatrix), C = elements x heads.  mma.sync m16n8k16 holds 8
+// heads without padding its 16-row side; one tcgen05 instruction wants 64 or
+// 128 rows of A and both products' operands staged through shared or tensor
+// memory, which a few query heads over codes that have to be converted in
+// registers do not pay for.
+//   4- and 8-bit codes become exact fp16 integers: a code under the exponent of
+//     1024 is 1024 + q, and the subtraction is exact.  Queries are scaled per
+//     head by a power of two that brings the largest to [2^14, 2^15), exact in
+//     fp16 for every bf16 within 2^28 of it.  p * scale is rounded once to fp16
+//     (2^-11), after a power of two, common to a warp's slots, that brings the
+//     largest scale so far to about 2^9 (terms below 2^-33 of it lose bits).
+//   bf16 rows are multiplied as they are, p rounded once to bf16 (2^-8).
+//   Sums are fp32 throughout.
+// The k index of a product may be any permutation of its 16 elements or slots
+// as long as both operands agree: it is chosen so that a 32-bit word of codes
+// yields whole operand registers (elements (0,4), (1,5), (2,6), (3,7) of a word
+// of 4-bit codes) and shared-memory reads meet all 32 banks.
+//
+// Work.  All (sequence, kv head, 8 or 16 query heads) segments are cut into
+// tiles of 16 or 32 slots, numbered through, and shared out evenly over all
+// warps of the grid, whatever the lengths: a warp walks a contiguous range with
+// a ring of tiles of its own in shared memory, filled by 16-byte cp.async a few
+// tiles ahead, and needs no barrier but its own until its range is done.  A
+// segment inside a warp's range is written out by it; pieces of a segment are
+// joined within the CTA, and those of CTAs by a second kernel, in order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "qmv_kv.h"
+
+namespace qmvc {
+
+struct AttnParams {
+  CacheView c;
+  const __nv_bfloat16 *q;
+  long long q_stride;
+  const int *lens;
+  __nv_bfloat16 *out;
+  int batch, Hq, R;
+  int chunks;          // segments of a kv head: ceil(R / heads of a segment)
+  float scale_log2;    // scale * log2(e)
+  float *weights;      // or null
+  int state_width;
+  long long room;
+  // workspace
+  int *cum;            // [batch + 1] tiles before a sequence
+  float *scores;       // [batch][Hq][room], with weights
+  float2 *stats;       // [batch][Hq] maximum and sum of segments not joined by the second kernel
+  float2 *part_ml;     // [ctas][2][heads]
+  float *part_o;       // [ctas][2][heads][D]
+  float *warp_o;       // [ctas][warps][heads][D]
+  int ctas;
+};
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLazy = 3.0f;  // p <= 2^kLazy
+
+template <int BITS_, int D_, int GS_, int NB_>
+struct AttnCfg {
+  static constexpr int BITS = BITS_, D = D_, GS = BITS_ == 16 ? D_ : GS_, NB = NB_;
+  static constexpr int HEADS = 8 * NB;                 // query heads of a segment
+  static constexpr int G = BITS == 16 ? 0 : D / GS;    // groups of a row
+  static constexpr int RB = D * BITS / 8;              // bytes of a row
+  static constexpr int CH = RB / 16;                   // 16-byte chunks of a row
+  // accumulators of at most 32 registers leave room for 16 warps on an SM
+  static constexpr bool SMALL = D * NB <= 128 && BITS != 16;
+  static constexpr int WARPS = BITS == 16 && D == 256 ? 4 : 8;
+  static constexpr int CTAS_PER_SM = SMALL ? 2 : 1;
+  static constexpr int ROOM = (SMALL ? 110592 : 204800) / WARPS;  // bytes of a warp's ring
+  // 4-bit tiles are 32 slots where three of them fit: half as many softmax
+  // steps for the same bytes
+  static constexpr int SLOT = 2 * RB + 8 * G;          // bytes of a slot
+  static constexpr int TB = BITS == 4 && SMALL && 3 * 32 * SLOT <= ROOM ? 2 : 1;  // 16-slot blocks
+  static constexpr int TILE = 16 * TB;
+  static constexpr int STAGE = TILE * SLOT;
+  static constexpr int RING = ROOM / STAGE;
+  static constexpr int STAGES = RING < 6 ? RING : 6;
+  static_assert(STAGES >= 2, "a tile is fetched while another is computed");
+  static constexpr int TAIL = HEADS * D * 4;           // a warp's last piece
+  static constexpr int SMEM = WARPS * (STAGES * STAGE > TAIL ? STAGES * STAGE : TAIL);
+  static constexpr int MT = D / 16;                    // 16-element accumulator tiles
+  // elements that one set of value words covers
+  static constexpr int VCH = BITS == 4 && GS >= 64 ? 64 : 32;
+};
+
+// Chunk swizzle of row r and the slot that product row r stands for, chosen
+// per row size so that the score reads (8 rows, one chunk) and the value reads
+// (4 rows, two chunks) each meet all banks.
+template <int CH>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (CH == 2 || CH == 6) return (r >> 2) & 1;
+  else if constexpr (CH == 4 || CH == 12) return (r >> 1) & 3;
+  else if constexpr (CH == 3) return 0;
+  else return r & 7;
+}
+template <int CH>
+__device__ __forceinline__ int slot_of(int r) {  // r < 8
+  if constexpr (CH == 2) return ((r & 1) << 2) | (r >> 1);
+  else if constexpr (CH == 4) return (r & 4) | ((r & 1) << 1) | ((r >> 1) & 1);
+  else return r;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_s32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
+  return v;
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) {  // e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+__device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ __half2 as_half2(uint32_t v) {
+  return *reinterpret_cast<const __half2 *>(&v);
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (BF16) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  } else {
+    return as_u32(__floats2half2_rn(lo, hi));
+  }
+}
+
+// Nibbles (j, j + 4) of x's 16-bit halves (j = 0 .. 3) as exact fp16 pairs.
+__device__ __forceinline__ void nibbles(uint32_t x, uint32_t (&o)[4]) {
+  const __half2 k1024 = as_half2(0x64006400u), sixteenth = as_half2(0x2c002c00u),
+                m64 = as_half2(0xd400d400u);
+  const uint32_t y = x >> 8;
+  o[0] = as_u32(__hsub2(as_half2((x & 0x000f000fu) | 0x64006400u), k1024));
+  o[1] = as_u32(__hfma2(as_half2((x & 0x00f000f0u) | 0x64006400u), sixteenth, m64));
+  o[2] = as_u32(__hsub2(as_half2((y & 0x000f000fu) | 0x64006400u), k1024));
+  o[3] = as_u32(__hfma2(as_half2((y & 0x00f000f0u) | 0x64006400u), sixteenth, m64));
+}
+// Bytes (0, 1) or (2, 3) of x as an exact fp16 pair.
+template <int PAIR>
+__device__ __forceinline__ uint32_t bytes16(uint32_t x) {
+  const uint32_t v = __byte_perm(x, 0x64646464u, PAIR ? 0x4342 : 0x4140);
+  return as_u32(__hsub2(as_half2(v), as_half2(0x64006400u)));
+}
+
+// G bf16 values at shared address a, as pairs of bits.
+template <int G>
+__device__ __forceinline__ void ld_groups(uint32_t a, uint32_t (&v)[(G + 1) / 2]) {
+  if constexpr (G == 1) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(x) : "r"(a));
+    v[0] = x;
+  } else if constexpr (G == 2) {
+    v[0] = ld_s32(a);
+  } else if constexpr (G == 3) {  // heads of 96: 6 bytes, 2-byte aligned
+    uint16_t x[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(x[i]) : "r"(a + 2 * i));
+    v[0] = x[0] | (static_cast<uint32_t>(x[1]) << 16);
+    v[1] = x[2];
+  } else if constexpr (G == 4) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+  } else {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+  }
+}
+__device__ __forceinline__ float group_value(const uint32_t *v, int g) {
+  return (g & 1) ? __uint_as_float(v[g / 2] & 0xffff0000u) : __uint_as_float(v[g / 2] << 16);
+}
+
+// Element of accumulator tile mt, product row lane/4 + 8*half.
+template <class C>
+__device__ __forceinline__ int element_of(int mt, int half, int g) {
+  if constexpr (C::BITS == 16) return 16 * mt + g + 8 * half;
+  else if constexpr (C::BITS == 8) return 32 * (mt / 2) + 4 * g + 2 * half + mt % 2;
+  else if constexpr (C::VCH == 64) return 64 * (mt / 4) + 8 * g + 4 * half + mt % 4;
+  else return 32 * (mt / 2) + 8 * (g & 3) + 4 * (g >> 2) + 2 * half + mt % 2;
+}
+
+__device__ __forceinline__ int clipped_length(const AttnParams &p, int b) {
+  const int len = __ldg(p.lens + b);
+  return len < 0 ? 0 : len < p.room ? len : static_cast<int>(p.room);
+}
+
+// The CTA whose warps hold tile u, when `total` tiles are shared out over
+// `warps` warps (warp i takes tiles [i * total / warps, (i + 1) * total / warps)).
+__device__ __forceinline__ int warp_of_tile(long long u, long long total, long long warps) {
+  return static_cast<int>(((u + 1) * warps - 1) / total);
+}
+
+// CTAs that take part: every one, or fewer where each warp would have less
+// than one tile.
+__device__ __forceinline__ int active_ctas(long long total, int ctas, int warps) {
+  const long long need = (total + warps - 1) / warps;
+  return static_cast<int>(need < ctas ? need : ctas);
+}
+
+// Position in the numbered tiles.
+struct Cursor {
+  int b, hc, tile, tiles, n;  // sequence, segment within it, tile, tiles of a segment, slots
+};
+
+template <class C>
+__device__ __forceinline__ void cursor_sequence(const AttnParams &p, Cursor &k) {
+  k.n = clipped_length(p, k.b);
+  k.tiles = (k.n + C::TILE - 1) / C::TILE;
+}
+
+template <class C>
+__device__ __forceinline__ Cursor cursor_at(const AttnParams &p, const int *cum, int u) {
+  int lo = 0, hi = p.batch;  // cum[lo] <= u < cum[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  Cursor k;
+  k.b = lo;
+  cursor_sequence<C>(p, k);
+  const int rest = u - cum[lo];
+  k.hc = rest / k.tiles;
+  k.tile = rest - k.hc * k.tiles;
+  return k;
+}
+
+// True when the next tile is another segment's.
+template <class C>
+__device__ __forceinline__ bool cursor_next(const AttnParams &p, const int *cum, Cursor &k) {
+  if (++k.tile < k.tiles) return false;
+  k.tile = 0;
+  if (++k.hc == p.c.H * p.chunks) {
+    k.hc = 0;
+    do ++k.b;
+    while (k.b < p.batch && cum[k.b + 1] == cum[k.b]);
+    if (k.b < p.batch) cursor_sequence<C>(p, k);
+  }
+  return true;
+}
+
+// What a warp carries through a segment.  Lane (g, t) = (lane / 4, lane % 4)
+// has heads 2t and 2t + 1 of each block of 8.
+template <class C>
+struct Segment {
+  uint32_t q[C::NB][C::D / 8];                       // B operands of the scores
+  float x[C::G ? C::G : 1][C::NB][2];                // sums of a group's queries
+  float f[C::NB][2];                                 // score units of a head
+  float o[C::MT][C::NB][4];
+  float m[C::NB][2], l[C::NB][2];
+  float pb[C::G ? C::G : 1][C::NB][2];               // sums of p * bias
+  float limit;                                       // largest scale for the current power
+  int vexp;                                          // values are scaled by 2^vexp
+
+  __device__ __forceinline__ void start(const AttnParams &p, const Cursor &k, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int hk = k.hc / p.chunks, ch = k.hc - hk * p.chunks;
+    // the same power of two for every group of sums below
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+      const int r = ch * C::HEADS + nb * 8 + g;
+      const bool live = r < p.R;
+      const __nv_bfloat16 *row = p.q + k.b * p.q_stride + (hk * p.R + (live ? r : 0)) * C::D;
+      if constexpr (C::BITS == 16) {
+#pragma unroll
+        for (int i = 0; i < C::D / 16; ++i) {
+          const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * i + 2 * t);
+          q[nb][2 * i] = live ? __ldg(w) : 0u;
+          q[nb][2 * i + 1] = live ? __ldg(w + 4) : 0u;
+        }
+        f[nb][0] = f[nb][1] = p.scale_log2;
+      } else {
+        // this lane's elements: of word t + 4 i, 8 (4-bit) or 4 (8-bit codes)
+        constexpr int PER = 32 / C::BITS, STEPS = C::D / (4 * PER);
+        uint32_t raw[STEPS][PER / 2];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const __nv_bfloat16 *w = row + PER * (t + 4 * i);
+          if constexpr (PER == 8) {
+            const uint4 v = live ? __ldg(reinterpret_cast<const uint4 *>(w)) : make_uint4(0, 0, 0, 0);
+            raw[i][0] = v.x; raw[i][1] = v.y; raw[i][2] = v.z; raw[i][3] = v.w;
+          } else {
+            const uint2 v = live ? __ldg(reinterpret_cast<const uint2 *>(w)) : make_uint2(0, 0);
+            raw[i][0] = v.x; raw[i][1] = v.y;
+          }
+#pragma unroll
+          for (int j = 0; j < PER / 2; ++j)
+            top = max(top, max(raw[i][j] & 0x7fffu, (raw[i][j] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e brings the largest to [2^14, 2^15); -114 <= e <= 126 keeps 2^e normal
+        int e = top >= 0x80u ? 14 - (static_cast<int>(top >> 7) - 127) : 126;
+        e = e > 126 ? 126 : e;
+        const float up = pow2(e);
+        float sums[C::G];
+#pragma unroll
+        for (int i = 0; i < C::G; ++i) sums[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          float v[PER];
+#pragma unroll
+          for (int j = 0; j < PER / 2; ++j) {
+            v[2 * j] = __uint_as_float(raw[i][j] << 16) * up;
+            v[2 * j + 1] = __uint_as_float(raw[i][j] & 0xffff0000u) * up;
+          }
+          if constexpr (PER == 8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[nb][4 * i + j] = pack16<false>(v[j], v[j + 4]);
+          } else {
+            q[nb][2 * i] = pack16<false>(v[0], v[1]);
+            q[nb][2 * i + 1] = pack16<false>(v[2], v[3]);
+          }
+#pragma unroll
+          for (int j = 0; j < PER; ++j) sums[i * 4 * PER / C::GS] += v[j];
+        }
+        const float unit = p.scale_log2 * pow2(-e);
+#pragma unroll
+        for (int i = 0; i < C::G; ++i) {
+          sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 1);
+          sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 2);
+          // head h's sums are in lanes 4 h .. 4 h + 3
+          x[i][nb][0] = __shfl_sync(0xffffffffu, sums[i], 8 * t);
+          x[i][nb][1] = __shfl_sync(0xffffffffu, sums[i], 8 * t + 4);
+        }
+        f[nb][0] = __shfl_sync(0xffffffffu, unit, 8 * t);
+        f[nb][1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4);
+      }
+      m[nb][0] = m[nb][1] = kNegInf;
+      l[nb][0] = l[nb][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nb][j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C::G; ++i) pb[i][nb][0] = pb[i][nb][1] = 0.0f;
+    }
+    vexp = 126;
+    limit = 4096.0f * pow2(-126);
+  }
+
+  // The sums over all lanes of the warp: l, and the values in true units.
+  __device__ __forceinline__ void finish() {
+    const float back = C::BITS == 16 ? 1.0f : pow2(-vexp);
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], s);
+        if constexpr (C::BITS != 16) {
+#pragma unroll
+          for (int g = 0; g < C::G; ++g)
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1)
+              pb[g][nb][i] += __shfl_xor_sync(0xffffffffu, pb[g][nb][i], s);
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt) {
+            const int g = mt * 16 / C::GS;
+            o[mt][nb][i] = fmaf(o[mt][nb][i], back, pb[g][nb][i]);
+            o[mt][nb][i + 2] = fmaf(o[mt][nb][i + 2], back, pb[g][nb][i]);
+          }
+        }
+      }
+  }
+};
+
+// One tile's scores, softmax step and value products.
+template <class C>
+__device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p, const Cursor &k,
+                                            uint32_t stage, uint32_t bad, int lane) {
+  constexpr bool BF = C::BITS == 16;
+  constexpr int GW = C::G ? (C::G + 1) / 2 : 1;
+  const int g = lane >> 2, t = lane & 3;
+  const int row = slot_of<C::CH>(g), sw = swizzle<C::CH>(row);
+  const uint32_t kbase = stage, vbase = stage + C::TILE * C::RB;
+  const uint32_t sbase = stage + 2 * C::TILE * C::RB;
+  constexpr uint32_t kArr = C::TILE * C::G * 2;
+  float s[C::TB][C::NB][4];
+
+#pragma unroll
+  for (int blk = 0; blk < C::TB; ++blk) {
+    const uint32_t kb = kbase + blk * 16 * C::RB;
+    if constexpr (BF) {
+      float c[C::NB][4] = {};
+      const uint32_t a0 = kb + (lane & 15) * C::RB;
+#pragma unroll
+      for (int i = 0; i < C::D / 16; ++i) {
+        uint32_t a[4];
+        ldmatrix4<false>(a, a0 + (((2 * i + (lane >> 4)) ^ swizzle<C::CH>(lane & 7)) << 4));
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb)
+          mma<true>(c[nb], a[0], a[1], a[2], a[3], sg.q[nb][2 * i], sg.q[nb][2 * i + 1]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[blk][nb][j] = c[nb][j] * sg.f[nb][j & 1];
+    } else {
+      uint32_t ska[GW], skb[GW], bka[GW], bkb[GW];
+      const uint32_t sa = sbase + (blk * 16 + row) * C::G * 2;
+      ld_groups<C::G>(sa, ska);
+      ld_groups<C::G>(sa + 16 * C::G, skb);
+      ld_groups<C::G>(sa + kArr, bka);
+      ld_groups<C::G>(sa + kArr + 16 * C::G, bkb);
+#pragma unroll
+      for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[blk][nb][j] = 0.0f;
+      constexpr int SPAN = C::BITS == 4 ? 32 : 16;  // elements of four lanes' words
+      constexpr int PER_GROUP = C::GS / SPAN;
+      const uint32_t ka = kb + row * C::RB + 4 * t;
+#pragma unroll
+      for (int gr = 0; gr < C::G; ++gr) {
+        float c[C::NB][4] = {};
+#pragma unroll
+        for (int ii = 0; ii < PER_GROUP; ++ii) {
+          const int i = gr * PER_GROUP + ii;
+          const uint32_t at = ka + ((i ^ sw) << 4);
+          const uint32_t w0 = ld_s32(at), w1 = ld_s32(at + 8 * C::RB);
+          if constexpr (C::BITS == 4) {
+            uint32_t u[4], v[4];
+            nibbles(w0, u);
+            nibbles(w1, v);
+#pragma unroll
+            for (int nb = 0; nb < C::NB; ++nb) {
+              mma<false>(c[nb], u[0], v[0], u[1], v[1], sg.q[nb][4 * i], sg.q[nb][4 * i + 1]);
+              mma<false>(c[nb], u[2], v[2], u[3], v[3], sg.q[nb][4 * i + 2], sg.q[nb][4 * i + 3]);
+            }
+          } else {
+            const uint32_t u0 = bytes16<0>(w0), u1 = bytes16<1>(w0);
+            const uint32_t v0 = bytes16<0>(w1), v1 = bytes16<1>(w1);
+#pragma unroll
+            for (int nb = 0; nb < C::NB; ++nb)
+              mma<false>(c[nb], u0, v0, u1, v1, sg.q[nb][2 * i], sg.q[nb][2 * i + 1]);
+          }
+        }
+        const float s0 = group_value(ska, gr), s1 = group_value(skb, gr);
+        const float b0 = group_value(bka, gr), b1 = group_value(bkb, gr);
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[blk][nb][j] = fmaf(j < 2 ? s0 : s1, c[nb][j],
+                                 fmaf(j < 2 ? b0 : b1, sg.x[gr][nb][j & 1], s[blk][nb][j]));
+      }
+#pragma unroll
+      for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[blk][nb][j] *= sg.f[nb][j & 1];
+    }
+  }
+
+  // slots past the sequence's, or of a bad page, take no part
+  const int t0 = k.tile * C::TILE;
+  if (bad || t0 + C::TILE > k.n) {
+#pragma unroll
+    for (int blk = 0; blk < C::TB; ++blk)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (((bad >> blk) & 1u) || t0 + 16 * blk + row + 8 * (j >> 1) >= k.n)
+#pragma unroll
+          for (int nb = 0; nb < C::NB; ++nb) s[blk][nb][j] = kNegInf;
+  }
+  if (p.scores) {
+    const int hk = k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS;
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = r0 + nb * 8 + 2 * t + (j & 1);
+        if (r < p.R) {
+          float *to = p.scores + (static_cast<long long>(k.b) * p.Hq + hk * p.R + r) * p.room + t0;
+#pragma unroll
+          for (int blk = 0; blk < C::TB; ++blk) {
+            const int at = 16 * blk + row + 8 * (j >> 1);
+            if (t0 + at < k.n) to[at] = s[blk][nb][j];
+          }
+        }
+      }
+  }
+
+  // running maximum, and the scales' power of two
+  float top[C::NB][2];
+  bool raise = false;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x = fmaxf(s[0][nb][i], s[0][nb][i + 2]);
+      if constexpr (C::TB == 2) x = fmaxf(x, fmaxf(s[1][nb][i], s[1][nb][i + 2]));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      top[nb][i] = x;
+      raise |= x > sg.m[nb][i] + kLazy;
+    }
+  uint32_t sva[C::TB][GW], svb[C::TB][GW];
+  float large = 0.0f;
+  if constexpr (!BF) {
+#pragma unroll
+    for (int blk = 0; blk < C::TB; ++blk) {
+      const uint32_t a = sbase + 2 * kArr + (blk * 16 + row) * C::G * 2;
+      ld_groups<C::G>(a, sva[blk]);
+      ld_groups<C::G>(a + 16 * C::G, svb[blk]);
+#pragma unroll
+      for (int gr = 0; gr < C::G; ++gr)
+        large = fmaxf(large, fmaxf(fabsf(group_value(sva[blk], gr)), fabsf(group_value(svb[blk], gr))));
+    }
+    raise |= large > sg.limit;
+  }
+  if (__any_sync(0xffffffffu, raise)) {
+    float ratio = 1.0f;
+    if constexpr (!BF) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, o));
+      if (large > sg.limit) {
+        int e = 9 - (static_cast<int>(__float_as_uint(large) >> 23) - 127);
+        e = e > 126 ? 126 : e < -118 ? -118 : e;
+        const int step = e - sg.vexp;  // below 0
+        ratio = step < -126 ? 0.0f : pow2(step);
+        sg.vexp = e;
+        sg.limit = 4096.0f * pow2(-e);
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float m = fmaxf(sg.m[nb][i], top[nb][i]);
+        const float a = m == kNegInf ? 1.0f : ex2(sg.m[nb][i] - m);
+        sg.m[nb][i] = m;
+        sg.l[nb][i] *= a;
+#pragma unroll
+        for (int gr = 0; gr < C::G; ++gr) sg.pb[gr][nb][i] *= a;
+        const float ar = a * ratio;
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) {
+          sg.o[mt][nb][i] *= ar;
+          sg.o[mt][nb][i + 2] *= ar;
+        }
+      }
+  }
+  const float power = BF ? 1.0f : pow2(sg.vexp);
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float m = sg.m[nb][i] == kNegInf ? 0.0f : sg.m[nb][i];
+#pragma unroll
+      for (int blk = 0; blk < C::TB; ++blk)
+#pragma unroll
+        for (int j = i; j < 4; j += 2) {
+          s[blk][nb][j] = ex2(s[blk][nb][j] - m);
+          sg.l[nb][i] += s[blk][nb][j];
+        }
+    }
+
+  // values
+#pragma unroll
+  for (int blk = 0; blk < C::TB; ++blk) {
+    const uint32_t vb = vbase + blk * 16 * C::RB;
+    if constexpr (BF) {
+      uint32_t b[C::NB][2];
+#pragma unroll
+      for (int nb = 0; nb < C::NB; ++nb) {
+        b[nb][0] = movmatrix(pack16<true>(s[blk][nb][0], s[blk][nb][1]));
+        b[nb][1] = movmatrix(pack16<true>(s[blk][nb][2], s[blk][nb][3]));
+      }
+      const int r = (lane & 7) + ((lane >> 4) << 3);
+      const uint32_t a0 = vb + r * C::RB;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
+        uint32_t a[4];
+        ldmatrix4<true>(a, a0 + (((2 * mt + ((lane >> 3) & 1)) ^ swizzle<C::CH>(lane & 7)) << 4));
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb)
+          mma<true>(sg.o[mt][nb], a[0], a[1], a[2], a[3], b[nb][0], b[nb][1]);
+      }
+    } else {
+      uint32_t bva[GW], bvb[GW];
+      const uint32_t ba = sbase + 3 * kArr + (blk * 16 + row) * C::G * 2;
+      ld_groups<C::G>(ba, bva);
+      ld_groups<C::G>(ba + 16 * C::G, bvb);
+      // the four slots of this lane's operand columns, and their rows
+      const int ra = slot_of<C::CH>(2 * t), rb = slot_of<C::CH>(2 * t + 1);
+      const int xa = swizzle<C::CH>(ra), xb = swizzle<C::CH>(rb);
+      const uint32_t va = vb + ra * C::RB, vc = vb + rb * C::RB;
+#pragma unroll
+      for (int gr = 0; gr < C::G; ++gr) {
+        uint32_t b[C::NB][2];
+        const float s0 = group_value(sva[blk], gr) * power, s1 = group_value(svb[blk], gr) * power;
+        const float b0 = group_value(bva, gr), b1 = group_value(bvb, gr);
+#pragma unroll
+        for (int nb = 0; nb < C::NB; ++nb) {
+          const float(&x)[4] = s[blk][nb];
+          b[nb][0] = movmatrix(pack16<false>(x[0] * s0, x[1] * s0));
+          b[nb][1] = movmatrix(pack16<false>(x[2] * s1, x[3] * s1));
+          sg.pb[gr][nb][0] += x[0] * b0 + x[2] * b1;
+          sg.pb[gr][nb][1] += x[1] * b0 + x[3] * b1;
+        }
+#pragma unroll
+        for (int cc = 0; cc < C::GS / C::VCH; ++cc) {
+          const int c = gr * (C::GS / C::VCH) + cc;
+          const int word = C::BITS == 8 ? 8 * c + g : C::VCH == 64 ? 8 * c + g : 4 * c + (g & 3);
+          const uint32_t oa = (((word >> 2) ^ xa) << 4) + ((word & 3) << 2);
+          const uint32_t ob = (((word >> 2) ^ xb) << 4) + ((word & 3) << 2);
+          const uint32_t w0 = ld_s32(va + oa), w1 = ld_s32(vc + ob);
+          const uint32_t w2 = ld_s32(va + oa + 8 * C::RB), w3 = ld_s32(vc + ob + 8 * C::RB);
+          if constexpr (C::BITS == 8) {
+            const uint32_t e0 = __byte_perm(w0, w1, 0x5140), e1 = __byte_perm(w0, w1, 0x7362);
+            const uint32_t e2 = __byte_perm(w2, w3, 0x5140), e3 = __byte_perm(w2, w3, 0x7362);
+            const uint32_t u0 = bytes16<0>(e0), u1 = bytes16<1>(e0), u2 = bytes16<0>(e1), u3 = bytes16<1>(e1);
+            const uint32_t z0 = bytes16<0>(e2), z1 = bytes16<1>(e2), z2 = bytes16<0>(e3), z3 = bytes16<1>(e3);
+#pragma unroll
+            for (int nb = 0; nb < C::NB; ++nb) {
+              mma<false>(sg.o[2 * c][nb], u0, u2, z0, z2, b[nb][0], b[nb][1]);
+              mma<false>(sg.o[2 * c + 1][nb], u1, u3, z1, z3, b[nb][0], b[nb][1]);
+            }
+          } else if constexpr (C::VCH == 64) {
+            uint32_t u[4], v[4], y[4], z[4];
+            nibbles(__byte_perm(w0, w1, 0x5410), u);
+            nibbles(__byte_perm(w0, w1, 0x7632), v);
+            nibbles(__byte_perm(w2, w3, 0x5410), y);
+            nibbles(__byte_perm(w2, w3, 0x7632), z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int nb = 0; nb < C::NB; ++nb)
+                mma<false>(sg.o[4 * c + j][nb], u[j], v[j], y[j], z[j], b[nb][0], b[nb][1]);
+          } else {
+            const uint32_t sel = g < 4 ? 0x5410u : 0x7632u;
+            uint32_t u[4], y[4];
+            nibbles(__byte_perm(w0, w1, sel), u);
+            nibbles(__byte_perm(w2, w3, sel), y);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int nb = 0; nb < C::NB; ++nb)
+                mma<false>(sg.o[2 * c + j][nb], u[j], u[j + 2], y[j], y[j + 2], b[nb][0], b[nb][1]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Fetches tiles ahead of the computation.
+template <class C>
+struct Fetcher {
+  Cursor k;
+  int page_at, in_page;        // page of the sequence, and 16-slot block within it
+  int pages[C::TB];            // looked up one tile ahead
+  int left;                    // tiles still to fetch
+  const uint16_t *scales[(8 * C::G + 31) / 32 ? (8 * C::G + 31) / 32 : 1];
+
+  __device__ __forceinline__ void start(const AttnParams &p, const Cursor &at, int count, int lane) {
+    k = at;
+    left = count;
+    if constexpr (C::BITS != 16) {
+#pragma unroll
+      for (int i = 0; i < (8 * C::G + 31) / 32; ++i) {
+        const int a = (lane + 32 * i) / (2 * C::G);
+        scales[i] = a == 0 ? p.c.k_scales : a == 1 ? p.c.k_biases : a == 2 ? p.c.v_scales : p.c.v_biases;
+      }
+    }
+    if (left > 0) place(p);
+  }
+  __device__ __forceinline__ void place(const AttnParams &p) {
+    const int blk = k.tile * C::TB, per = p.c.S / 16;
+    page_at = blk / per;
+    in_page = blk - page_at * per;
+    look_up(p);
+  }
+  __device__ __forceinline__ void look_up(const AttnParams &p) {
+    const int *row = p.c.table + static_cast<long long>(k.b) * p.c.width;
+    const int per = p.c.S / 16;
+    int at = page_at, in = in_page;
+#pragma unroll
+    for (int i = 0; i < C::TB; ++i) {
+      // a block past the sequence's slots is not looked up
+      pages[i] = k.tile * C::TILE + 16 * i < k.n ? __ldg(row + at) : -1;
+      if (++in == per) {
+        in = 0;
+        ++at;
+      }
+    }
+  }
+  // Starts the copies of the next tile; returns the blocks of bad pages.
+  __device__ __forceinline__ uint32_t fetch(const AttnParams &p, const int *cum, uint32_t stage,
+                                            int lane) {
+    uint32_t bad = 0u;
+    if (left > 0) {
+      const int hk = k.hc / p.chunks, per = p.c.S / 16;
+      int in = in_page;
+#pragma unroll
+      for (int i = 0; i < C::TB; ++i) {
+        const int have = k.n - (k.tile * C::TILE + 16 * i);  // valid slots of the block
+        int page = pages[i];
+        int rows = have < 0 ? 0 : have < 16 ? have : 16;
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
+          if (rows > 0) {
+            bad |= 1u << i;
+            if (p.c.status && lane == 0) atomicOr(p.c.status, 1);
+          }
+          rows = 0;
+          page = 0;
+        }
+        const long long first = cache_row(p.c, page, hk, 16 * in);
+        const uint8_t *ks = p.c.k + first * C::RB + lane * 16, *vs = p.c.v + first * C::RB + lane * 16;
+#pragma unroll
+        for (int c = 0; c < (C::CH + 1) / 2; ++c) {
+          const int ix = c * 32 + lane;
+          const int r = ix / C::CH, col = ix - r * C::CH;
+          if (C::CH % 2 == 0 || ix < 16 * C::CH) {
+            const uint32_t to = (16 * i + r) * C::RB + ((col ^ swizzle<C::CH>(r)) << 4);
+            const int bytes = r < rows ? 16 : 0;
+            cp_async16(stage + to, ks + c * 512, bytes);
+            cp_async16(stage + C::TILE * C::RB + to, vs + c * 512, bytes);
+          }
+        }
+        if constexpr (C::BITS != 16) {
+#pragma unroll
+          for (int c = 0; c < (8 * C::G + 31) / 32; ++c) {
+            const int ix = c * 32 + lane;
+            if (ix < 8 * C::G) {
+              const int a = ix / (2 * C::G), j = ix - a * 2 * C::G;
+              int bytes = rows * C::G * 2 - j * 16;
+              bytes = bytes < 0 ? 0 : bytes < 16 ? bytes : 16;
+              cp_async16(stage + 2 * C::TILE * C::RB + a * C::TILE * C::G * 2 + i * 32 * C::G + j * 16,
+                         scales[c] + first * C::G + j * 8, bytes);
+            }
+          }
+        }
+        if (++in == per) in = 0;
+      }
+      if (--left > 0) {
+        if (cursor_next<C>(p, cum, k)) {
+          place(p);
+        } else {
+          in_page += C::TB;
+          while (in_page >= per) {
+            in_page -= per;
+            ++page_at;
+          }
+          look_up(p);
+        }
+      }
+    }
+    cp_commit();
+    return bad;
+  }
+};
+
+// out of one head: bf16 values from sums and 1 / l
+template <class C>
+__device__ __forceinline__ void write_out(const Segment<C> &sg, const AttnParams &p, const Cursor &k,
+                                          int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const int hk = k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + nb * 8 + 2 * t + i;
+      if (r >= p.R) continue;
+      const long long head = static_cast<long long>(k.b) * p.Hq + hk * p.R + r;
+      const float inv = sg.l[nb][i] > 0.0f ? 1.0f / sg.l[nb][i] : 0.0f;
+      __nv_bfloat16 *to = p.out + head * C::D;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
+        to[element_of<C>(mt, 0, g)] = __float2bfloat16_rn(sg.o[mt][nb][i] * inv);
+        to[element_of<C>(mt, 1, g)] = __float2bfloat16_rn(sg.o[mt][nb][i + 2] * inv);
+      }
+      if (p.scores && g == 0) p.stats[head] = make_float2(sg.m[nb][i], sg.l[nb][i]);
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void write_piece(const Segment<C> &sg, float *o, float2 *ml, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = nb * 8 + 2 * t + i;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
+        o[h * C::D + element_of<C>(mt, 0, g)] = sg.o[mt][nb][i];
+        o[h * C::D + element_of<C>(mt, 1, g)] = sg.o[mt][nb][i + 2];
+      }
+      if (g == 0) ml[h] = make_float2(sg.m[nb][i], sg.l[nb][i]);
+    }
+}
+
+// Tiles before every sequence, into shared memory (and the workspace, for the
+// second kernel).
+template <class C>
+__device__ __forceinline__ void sum_tiles(const AttnParams &p, int *cum, int threads) {
+  __shared__ int part[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch + threads - 1) / threads;
+  const int b0 = tid * per < p.batch ? tid * per : p.batch;
+  const int b1 = b0 + per < p.batch ? b0 + per : p.batch;
+  const int unit = p.c.H * p.chunks;
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (p.c.status && blockIdx.x == 0 && __ldg(p.lens + b) > p.room) atomicOr(p.c.status, 1);
+    sum += (clipped_length(p, b) + C::TILE - 1) / C::TILE * unit;
+  }
+  int before = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) part[warp] = before;
+  __syncthreads();
+  before -= sum;
+  for (int w = 0; w < warp; ++w) before += part[w];
+  for (int b = b0; b < b1; ++b) {
+    cum[b] = before;
+    if (blockIdx.x == 0) p.cum[b] = before;
+    before += (clipped_length(p, b) + C::TILE - 1) / C::TILE * unit;
+  }
+  if (b1 == p.batch && (b0 < b1 || tid == 0)) {
+    cum[p.batch] = before;
+    if (blockIdx.x == 0) p.cum[p.batch] = before;
+  }
+  __syncthreads();
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::WARPS * 32, C::CTAS_PER_SM)
+attn_kernel(const AttnParams p) {
+  extern __shared__ __align__(128) uint8_t attn_smem[];
+  __shared__ float2 piece_ml[2][C::WARPS][C::HEADS];  // first and last pieces
+  __shared__ int piece_seg[2][C::WARPS];              // segment, or -1
+  int *cum = reinterpret_cast<int *>(attn_smem + C::SMEM);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  wait_for_previous_grid();
+  sum_tiles<C>(p, cum, C::WARPS * 32);
+  const int total = cum[p.batch], unit = p.c.H * p.chunks;
+
+  // rows of sequences without slots
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (cum[b + 1] == cum[b]) {
+      uint4 *to = reinterpret_cast<uint4 *>(p.out + static_cast<long long>(b) * p.Hq * C::D);
+      for (int i = tid; i < p.Hq * C::D / 8; i += C::WARPS * 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  const int ctas = active_ctas(total, p.ctas, C::WARPS);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+
+  const long long warps = static_cast<long long>(ctas) * C::WARPS;
+  const long long me = static_cast<long long>(blockIdx.x) * C::WARPS + warp;
+  const int u0 = static_cast<int>(me * total / warps), u1 = static_cast<int>((me + 1) * total / warps);
+  const int c0 = static_cast<int>((me - warp) * total / warps);
+  const int c1 = static_cast<int>((me - warp + C::WARPS) * total / warps);
+  const uint32_t ring = smem_addr(attn_smem) + warp * C::STAGES * C::STAGE;
+  if (lane == 0) piece_seg[0][warp] = piece_seg[1][warp] = -1;
+
+  bool tail = false;
+  Segment<C> sg;
+  if (u0 < u1) {
+    Cursor k = cursor_at<C>(p, cum, u0);
+    Fetcher<C> fetch;
+    fetch.start(p, k, u1 - u0, lane);
+    uint32_t bad = 0u;  // TB bits for each stage of the ring
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i)
+      bad |= fetch.fetch(p, cum, ring + i * C::STAGE, lane) << (i * C::TB);
+    sg.start(p, k, lane);
+    int stage = 0, ahead = C::STAGES - 1, since = u0;  // first tile of the segment here
+    for (int u = u0; u < u1; ++u) {
+      cp_wait<C::STAGES - 2>();
+      __syncwarp();
+      {
+        const uint32_t mask = (1u << C::TB) - 1u;
+        const uint32_t b = fetch.fetch(p, cum, ring + ahead * C::STAGE, lane);
+        bad = (bad & ~(mask << (ahead * C::TB))) | (b << (ahead * C::TB));
+        attend_tile<C>(sg, p, k, ring + stage * C::STAGE, (bad >> (stage * C::TB)) & mask, lane);
+      }
+      __syncwarp();
+      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+      ahead = ahead + 1 == C::STAGES ? 0 : ahead + 1;
+      const bool last = k.tile + 1 == k.tiles;
+      if (last) {
+        sg.finish();
+        if (u + 1 - k.tiles >= u0) {  // the whole segment was here
+          write_out<C>(sg, p, k, lane);
+        } else {
+          write_piece<C>(sg, p.warp_o + me * C::HEADS * C::D, piece_ml[0][warp], lane);
+          if (lane == 0) piece_seg[0][warp] = k.b * unit + k.hc;
+        }
+        since = u + 1;
+        if (u + 1 < u1) {
+          cursor_next<C>(p, cum, k);
+          sg.start(p, k, lane);
+        }
+      } else {
+        ++k.tile;
+      }
+    }
+    if (since < u1) {  // the segment goes on in the next warp
+      tail = true;
+      sg.finish();
+      if (lane == 0) piece_seg[1][warp] = k.b * unit + k.hc;
+    }
+    cp_wait<0>();
+  }
+  let_next_grid_start();
+  __syncthreads();  // the rings are free
+  float *tails = reinterpret_cast<float *>(attn_smem);
+  if (tail) write_piece<C>(sg, tails + warp * C::HEADS * C::D, piece_ml[1][warp], lane);
+  __syncthreads();
+
+  // join the pieces of a segment, in the order of its slots
+  for (int i = 0; i < 2 * C::WARPS;) {
+    const int seg = piece_seg[i & 1][i >> 1];
+    if (seg < 0) {
+      ++i;
+      continue;
+    }
+    int end = i + 1;
+    while (end < 2 * C::WARPS && (piece_seg[end & 1][end >> 1] == seg || piece_seg[end & 1][end >> 1] < 0)) ++end;
+    const int b = seg / unit, hc = seg - b * unit;
+    const int tiles = (cum[b + 1] - cum[b]) / unit;
+    const int first = cum[b] + hc * tiles;
+    const bool whole = first >= c0 && first + tiles <= c1;
+    const int slot = first < c0 ? 0 : 1;
+    const int hk = hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
+    const long long part = (static_cast<long long>(blockIdx.x) * 2 + slot) * C::HEADS;
+    for (int e = tid; e < C::HEADS * C::D; e += C::WARPS * 32) {
+      const int h = e / C::D, d = e - h * C::D;
+      if (r0 + h >= p.R) break;
+      float m = kNegInf;
+      for (int j = i; j < end; ++j)
+        if (piece_seg[j & 1][j >> 1] == seg) m = fmaxf(m, piece_ml[j & 1][j >> 1][h].x);
+      const float ms = m == kNegInf ? 0.0f : m;
+      float l = 0.0f, o = 0.0f;
+      for (int j = i; j < end; ++j) {
+        if (piece_seg[j & 1][j >> 1] != seg) continue;
+        const float2 ml = piece_ml[j & 1][j >> 1][h];
+        const float a = ex2(ml.x - ms);
+        const float *from = (j & 1) ? tails + (j >> 1) * C::HEADS * C::D
+                                    : p.warp_o + (me - warp + (j >> 1)) * C::HEADS * C::D;
+        l += a * ml.y;
+        o += a * from[e];
+      }
+      const long long head = static_cast<long long>(b) * p.Hq + hk * p.R + r0 + h;
+      if (whole) {
+        p.out[head * C::D + d] = __float2bfloat16_rn(l > 0.0f ? o / l : 0.0f);
+        if (p.scores && d == 0) p.stats[head] = make_float2(m, l);
+      } else {
+        p.part_o[part * C::D + e] = o;
+        if (d == 0) p.part_ml[part + h] = make_float2(m, l);
+      }
+    }
+    i = end;
+  }
+}
+
+// CTAs that hold pieces of segment hc of sequence b: first and last, the same
+// where no second step is needed.
+template <class C>
+__device__ __forceinline__ int2 segment_ctas(const AttnParams &p, int b, int hc) {
+  const int total = p.cum[p.batch], unit = p.c.H * p.chunks;
+  const int tiles = (p.cum[b + 1] - p.cum[b]) / unit;
+  const int first = p.cum[b] + hc * tiles;
+  const long long warps = static_cast<long long>(active_ctas(total, p.ctas, C::WARPS)) * C::WARPS;
+  return make_int2(warp_of_tile(first, total, warps) / C::WARPS,
+                   warp_of_tile(first + tiles - 1, total, warps) / C::WARPS);
+}
+
+// Maximum and sum of one head over the CTAs that hold its segment.
+template <class C>
+__device__ __forceinline__ float2 joined_stats(const AttnParams &p, int2 at, int h) {
+  float m = kNegInf;
+  for (int c = at.x; c <= at.y; ++c)
+    m = fmaxf(m, p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h].x);
+  const float ms = m == kNegInf ? 0.0f : m;
+  float l = 0.0f;
+  for (int c = at.x; c <= at.y; ++c) {
+    const float2 ml = p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h];
+    l += ex2(ml.x - ms) * ml.y;
+  }
+  return make_float2(m, l);
+}
+
+constexpr int kWeightSlots = 1024;  // slots of a block that adds weights
+constexpr int kJoinThreads = 256;
+
+// Second kernel: a block per (sequence, query head) joins what several CTAs
+// hold; further blocks add a kv head's probabilities into the weights.
+template <class C>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int weight_blocks) {
+  const int tid = threadIdx.x;
+  wait_for_previous_grid();
+  const int heads = p.batch * p.Hq;
+  if (static_cast<int>(blockIdx.x) < heads) {
+    const int b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq;
+    if (p.cum[b + 1] == p.cum[b]) return;
+    const int hk = hq / p.R, r = hq - hk * p.R, ch = r / C::HEADS, h = r - ch * C::HEADS;
+    const int2 at = segment_ctas<C>(p, b, hk * p.chunks + ch);
+    if (at.x == at.y) return;
+    const float2 ml = joined_stats<C>(p, at, h);
+    const float ms = ml.x == kNegInf ? 0.0f : ml.x;
+    for (int d = tid; d < C::D; d += kJoinThreads) {
+      float o = 0.0f;
+      for (int c = at.x; c <= at.y; ++c) {
+        const long long i = (static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h;
+        o += ex2(p.part_ml[i].x - ms) * p.part_o[i * C::D + d];
+      }
+      p.out[static_cast<long long>(blockIdx.x) * C::D + d] =
+          __float2bfloat16_rn(ml.y > 0.0f ? o / ml.y : 0.0f);
+    }
+    return;
+  }
+  const int ix = blockIdx.x - heads, row = ix / weight_blocks, z = ix - row * weight_blocks;
+  const int b = row / p.c.H, hk = row - b * p.c.H;
+  const int n = clipped_length(p, b);
+  const int j0 = z * kWeightSlots;
+  if (j0 >= n) return;
+  const int j1 = j0 + kWeightSlots < n ? j0 + kWeightSlots : n;
+  __shared__ float2 ml[64];
+  float sum[kWeightSlots / kJoinThreads] = {};
+  for (int r0 = 0; r0 < p.R; r0 += 64) {
+    const int count = p.R - r0 < 64 ? p.R - r0 : 64;
+    __syncthreads();
+    if (tid < count) {
+      const int r = r0 + tid, ch = r / C::HEADS;
+      const int2 at = segment_ctas<C>(p, b, hk * p.chunks + ch);
+      ml[tid] = at.x == at.y ? p.stats[static_cast<long long>(b) * p.Hq + hk * p.R + r]
+                             : joined_stats<C>(p, at, r - ch * C::HEADS);
+    }
+    __syncthreads();
+    for (int r = 0; r < count; ++r) {
+      const float m = ml[r].x, inv = 1.0f / ml[r].y;
+      if (m == kNegInf) continue;  // no slot of the row takes part
+      const float *s = p.scores + (static_cast<long long>(b) * p.Hq + hk * p.R + r0 + r) * p.room;
+#pragma unroll
+      for (int i = 0; i < kWeightSlots / kJoinThreads; ++i) {
+        const int j = j0 + i * kJoinThreads + tid;
+        if (j < j1) sum[i] += ex2(s[j] - m) * inv;
+      }
+    }
+  }
+  float *w = p.weights + static_cast<long long>(row) * p.state_width;
+#pragma unroll
+  for (int i = 0; i < kWeightSlots / kJoinThreads; ++i) {
+    const int j = j0 + i * kJoinThreads + tid;
+    if (j < j1) w[j] += sum[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+template <class C>
+int attn_ctas(int sms) { return sms * C::CTAS_PER_SM; }
+
+// Lays the workspace out from `base` (null: only its size is wanted).
+template <class C>
+size_t lay_out(AttnParams &p, const CacheView &c, int batch, int num_q_heads, bool weights, int sms,
+               uint8_t *base) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t *r = base ? base + at : nullptr;
+    at += (bytes + 127) / 128 * 128;
+    return r;
+  };
+  const size_t ctas = attn_ctas<C>(sms), heads = static_cast<size_t>(batch) * num_q_heads;
+  p.cum = reinterpret_cast<int *>(take(4 * (static_cast<size_t>(batch) + 1)));
+  p.part_ml = reinterpret_cast<float2 *>(take(ctas * 2 * C::HEADS * 8));
+  p.part_o = reinterpret_cast<float *>(take(ctas * 2 * C::HEADS * C::D * 4));
+  p.warp_o = reinterpret_cast<float *>(take(ctas * C::WARPS * C::HEADS * C::D * 4));
+  if (weights) {
+    p.stats = reinterpret_cast<float2 *>(take(heads * 8));
+    p.scores = reinterpret_cast<float *>(take(heads * c.width * c.S * 4));
+  }
+  return at;
+}
+
+template <class C>
+cudaError_t attn_run(const AttnArgs &a, int sms) {
+  AttnParams p = {};
+  p.c = a.cache;
+  p.q = static_cast<const __nv_bfloat16 *>(a.q);
+  p.q_stride = a.q_stride;
+  p.lens = a.lens;
+  p.out = static_cast<__nv_bfloat16 *>(a.out);
+  p.batch = a.batch;
+  p.Hq = a.num_q_heads;
+  p.R = a.num_q_heads / a.cache.H;
+  p.chunks = (p.R + C::HEADS - 1) / C::HEADS;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.weights = a.weights;
+  p.state_width = a.state_width;
+  p.room = static_cast<long long>(a.cache.width) * a.cache.S;
+  p.ctas = attn_ctas<C>(sms);
+  lay_out<C>(p, a.cache, a.batch, a.num_q_heads, a.weights != nullptr, sms,
+             static_cast<uint8_t *>(a.workspace));
+  const size_t smem = C::SMEM + 4 * (static_cast<size_t>(a.batch) + 1);
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  e = launch_overlapped(attn_kernel<C>, dim3(p.ctas), C::WARPS * 32, smem, 1, a.stream, p);
+  if (e != cudaSuccess) return e;
+  const int weight_blocks =
+      a.weights ? static_cast<int>((p.room + kWeightSlots - 1) / kWeightSlots) : 0;
+  const long long blocks = static_cast<long long>(a.batch) * (p.Hq + static_cast<long long>(p.c.H) * weight_blocks);
+  return launch_overlapped(attn_join_kernel<C>, dim3(static_cast<unsigned>(blocks)), kJoinThreads, 0, 1,
+                           a.stream, p, weight_blocks);
+}
+
+// The kernel for a head size, group size and number of query heads to a kv
+// head: 16 heads at a time where there are more than 8 (but 8 for heads of
+// 256, whose accumulators fill the registers).
+template <int BITS, class F>
+auto attn_select(const CacheView &c, int R, F f) {
+  const int gs = BITS == 16 ? 32 : c.D / c.G;
+  const bool wide = R > 8;
+  if constexpr (BITS == 16) {
+    switch (c.D) {
+      case 64: return wide ? f(AttnCfg<16, 64, 64, 2>{}) : f(AttnCfg<16, 64, 64, 1>{});
+      case 96: return wide ? f(AttnCfg<16, 96, 96, 2>{}) : f(AttnCfg<16, 96, 96, 1>{});
+      case 128: return wide ? f(AttnCfg<16, 128, 128, 2>{}) : f(AttnCfg<16, 128, 128, 1>{});
+      default: return f(AttnCfg<16, 256, 256, 1>{});
+    }
+  } else {
+    switch (c.D) {
+      case 64:
+        if (gs == 32) return wide ? f(AttnCfg<BITS, 64, 32, 2>{}) : f(AttnCfg<BITS, 64, 32, 1>{});
+        return wide ? f(AttnCfg<BITS, 64, 64, 2>{}) : f(AttnCfg<BITS, 64, 64, 1>{});
+      case 96:
+        return wide ? f(AttnCfg<BITS, 96, 32, 2>{}) : f(AttnCfg<BITS, 96, 32, 1>{});
+      case 128:
+        if (gs == 32) return wide ? f(AttnCfg<BITS, 128, 32, 2>{}) : f(AttnCfg<BITS, 128, 32, 1>{});
+        if (gs == 64) return wide ? f(AttnCfg<BITS, 128, 64, 2>{}) : f(AttnCfg<BITS, 128, 64, 1>{});
+        return wide ? f(AttnCfg<BITS, 128, 128, 2>{}) : f(AttnCfg<BITS, 128, 128, 1>{});
+      default:
+        if (gs == 32) return f(AttnCfg<BITS, 256, 32, 1>{});
+        if (gs == 64) return f(AttnCfg<BITS, 256, 64, 1>{});
+        return f(AttnCfg<BITS, 256, 128, 1>{});
+    }
+  }
+}
+
+template <int BITS>
+size_t attn_workspace_bits(const CacheView &c, int batch, int num_q_heads, bool weights, int sms) {
+  return attn_select<BITS>(c, num_q_heads / c.H, [&](auto cfg) {
+    AttnParams p = {};
+    return lay_out<decltype(cfg)>(p, c, batch, num_q_heads, weights, sms, nullptr);
+  });
+}
+template <int BITS>
+cudaError_t attn_launch_bits(const AttnArgs &a, int sms) {
+  return attn_select<BITS>(a.cache, a.num_q_heads / a.cache.H,
+                           [&](auto cfg) { return attn_run<decltype(cfg)>(a, sms); });
+}
+
+}  // namespace qmvc
