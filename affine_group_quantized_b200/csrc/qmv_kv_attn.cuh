@@ -19,12 +19,13 @@
 // 128 rows of A and both products' operands staged through shared or tensor
 // memory, which a few query heads over codes that have to be converted in
 // registers do not pay for.
-//   4- and 8-bit codes become exact fp16 integers: a code under the exponent of
-//     1024 is 1024 + q, and the subtraction is exact.  Queries are scaled per
-//     head by a power of two that brings the largest to [2^14, 2^15), exact in
-//     fp16 for every bf16 within 2^28 of it.  p * scale is rounded once to fp16
-//     (2^-11), after a power of two, common to a warp's slots, that brings the
-//     largest scale so far to about 2^9 (terms below 2^-33 of it lose bits).
+//   4- and 8-bit codes are fp16 numbers already: the bits q alone are the
+//     subnormal q * 2^-24 (q * 2^-20 where a nibble stays in bits 4 .. 7, which
+//     its query element or output makes up for), exactly.  Queries are scaled
+//     per head by a power of two that brings the largest to [2^14, 2^15), exact
+//     in fp16 for every bf16 within 2^24 of it.  p * scale is rounded once to
+//     fp16 (2^-11), after a power of two, common to a warp's slots, that brings
+//     the largest scale so far to about 2^9 (terms below 2^-33 of it lose bits).
 //   bf16 rows are multiplied as they are, p rounded once to bf16 (2^-8).
 //   Sums are fp32 throughout.
 // The k index of a product may be any permutation of its 16 elements or slots
@@ -45,6 +46,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "qmv_kv.h"
@@ -59,7 +61,8 @@ struct AttnParams {
   __nv_bfloat16 *out;
   int batch, Hq, R;
   int chunks;          // segments of a kv head: ceil(R / heads of a segment)
-  float scale_log2;    // scale * log2(e)
+  float scale_log2;    // |scale| * log2(e)
+  uint32_t q_sign;     // flips the queries where scale is negative
   float *weights;      // or null
   int state_width;
   long long room;
@@ -119,6 +122,14 @@ __device__ __forceinline__ int slot_of(int r) {  // r < 8
   if constexpr (CH == 2) return ((r & 1) << 2) | (r >> 1);
   else if constexpr (CH == 4) return (r & 4) | ((r & 1) << 1) | ((r >> 1) & 1);
   else return r;
+}
+
+// Address of 16-byte chunk `chunk` (a constant) of a row, from that of its chunk
+// 0 (swizzled): the swizzle's bits are exchanged, the others added.
+template <int CH>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t row0, int chunk) {
+  constexpr int kBits = CH == 3 ? 0 : CH == 2 || CH == 6 ? 1 : CH == 4 || CH == 12 ? 3 : 7;
+  return (row0 ^ ((chunk & kBits) << 4)) + ((chunk & ~kBits) << 4);
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -189,22 +200,23 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// Nibbles (j, j + 4) of x's 16-bit halves (j = 0 .. 3) as exact fp16 pairs.
+// Codes as fp16 numbers without any conversion: the bits q alone are the fp16
+// subnormal q * 2^-24, exactly, and products take subnormals as they are.
+// Nibbles (j, j + 4) of x's 16-bit halves, j = 0 .. 3: q * 2^-24 for even j,
+// q * 2^-20 for odd j (bits 4 .. 7 of the fraction).
 __device__ __forceinline__ void nibbles(uint32_t x, uint32_t (&o)[4]) {
-  const __half2 k1024 = as_half2(0x64006400u), sixteenth = as_half2(0x2c002c00u),
-                m64 = as_half2(0xd400d400u);
   const uint32_t y = x >> 8;
-  o[0] = as_u32(__hsub2(as_half2((x & 0x000f000fu) | 0x64006400u), k1024));
-  o[1] = as_u32(__hfma2(as_half2((x & 0x00f000f0u) | 0x64006400u), sixteenth, m64));
-  o[2] = as_u32(__hsub2(as_half2((y & 0x000f000fu) | 0x64006400u), k1024));
-  o[3] = as_u32(__hfma2(as_half2((y & 0x00f000f0u) | 0x64006400u), sixteenth, m64));
+  o[0] = x & 0x000f000fu;
+  o[1] = x & 0x00f000f0u;
+  o[2] = y & 0x000f000fu;
+  o[3] = y & 0x00f000f0u;
 }
-// Bytes (0, 1) or (2, 3) of x as an exact fp16 pair.
+// Bytes (0, 1) or (2, 3) of x: q * 2^-24.
 template <int PAIR>
 __device__ __forceinline__ uint32_t bytes16(uint32_t x) {
-  const uint32_t v = __byte_perm(x, 0x64646464u, PAIR ? 0x4342 : 0x4140);
-  return as_u32(__hsub2(as_half2(v), as_half2(0x64006400u)));
+  return __byte_perm(x, 0u, PAIR ? 0x4342 : 0x4140);
 }
+constexpr float kUnit = 5.9604644775390625e-8f;  // 2^-24
 
 // G bf16 values at shared address a, as pairs of bits.
 template <int G>
@@ -328,8 +340,8 @@ struct Segment {
 #pragma unroll
         for (int i = 0; i < C::D / 16; ++i) {
           const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * i + 2 * t);
-          q[nb][2 * i] = live ? __ldg(w) : 0u;
-          q[nb][2 * i + 1] = live ? __ldg(w + 4) : 0u;
+          q[nb][2 * i] = live ? __ldg(w) ^ p.q_sign : 0u;
+          q[nb][2 * i + 1] = live ? __ldg(w + 4) ^ p.q_sign : 0u;
         }
         f[nb][0] = f[nb][1] = p.scale_log2;
       } else {
@@ -348,8 +360,10 @@ struct Segment {
             raw[i][0] = v.x; raw[i][1] = v.y;
           }
 #pragma unroll
-          for (int j = 0; j < PER / 2; ++j)
+          for (int j = 0; j < PER / 2; ++j) {
+            raw[i][j] ^= p.q_sign;
             top = max(top, max(raw[i][j] & 0x7fffu, (raw[i][j] >> 16) & 0x7fffu));
+          }
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -370,7 +384,10 @@ struct Segment {
           }
           if constexpr (PER == 8) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[nb][4 * i + j] = pack16<false>(v[j], v[j + 4]);
+            for (int j = 0; j < 4; ++j) {
+              const float odd = j & 1 ? 0.0625f : 1.0f;  // those nibbles count 16 times
+              q[nb][4 * i + j] = pack16<false>(v[j] * odd, v[j + 4] * odd);
+            }
           } else {
             q[nb][2 * i] = pack16<false>(v[0], v[1]);
             q[nb][2 * i + 1] = pack16<false>(v[2], v[3]);
@@ -378,14 +395,15 @@ struct Segment {
 #pragma unroll
           for (int j = 0; j < PER; ++j) sums[i * 4 * PER / C::GS] += v[j];
         }
-        const float unit = p.scale_log2 * pow2(-e);
+        // never 0, so that a masked score times it is -inf
+        const float unit = fmaxf(p.scale_log2 * pow2(-e) * (1.0f / kUnit), 1.17549435e-38f);
 #pragma unroll
         for (int i = 0; i < C::G; ++i) {
           sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 1);
           sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 2);
           // head h's sums are in lanes 4 h .. 4 h + 3
-          x[i][nb][0] = __shfl_sync(0xffffffffu, sums[i], 8 * t);
-          x[i][nb][1] = __shfl_sync(0xffffffffu, sums[i], 8 * t + 4);
+          x[i][nb][0] = __shfl_sync(0xffffffffu, sums[i] * kUnit, 8 * t);
+          x[i][nb][1] = __shfl_sync(0xffffffffu, sums[i] * kUnit, 8 * t + 4);
         }
         f[nb][0] = __shfl_sync(0xffffffffu, unit, 8 * t);
         f[nb][1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4);
@@ -421,8 +439,10 @@ struct Segment {
 #pragma unroll
           for (int mt = 0; mt < C::MT; ++mt) {
             const int g = mt * 16 / C::GS;
-            o[mt][nb][i] = fmaf(o[mt][nb][i], back, pb[g][nb][i]);
-            o[mt][nb][i + 2] = fmaf(o[mt][nb][i + 2], back, pb[g][nb][i]);
+            // 2^24, or 2^20 where the codes were those of odd nibbles
+            const float unit = C::BITS == 4 && mt % 2 ? 0.0625f / kUnit : 1.0f / kUnit;
+            o[mt][nb][i] = fmaf(o[mt][nb][i] * unit, back, pb[g][nb][i]);
+            o[mt][nb][i + 2] = fmaf(o[mt][nb][i + 2] * unit, back, pb[g][nb][i]);
           }
         }
       }
@@ -447,11 +467,11 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
     const uint32_t kb = kbase + blk * 16 * C::RB;
     if constexpr (BF) {
       float c[C::NB][4] = {};
-      const uint32_t a0 = kb + (lane & 15) * C::RB;
+      const uint32_t a0 = kb + (lane & 15) * C::RB + (((lane >> 4) ^ swizzle<C::CH>(lane & 7)) << 4);
 #pragma unroll
       for (int i = 0; i < C::D / 16; ++i) {
         uint32_t a[4];
-        ldmatrix4<false>(a, a0 + (((2 * i + (lane >> 4)) ^ swizzle<C::CH>(lane & 7)) << 4));
+        ldmatrix4<false>(a, chunk_at<C::CH>(a0, 2 * i));
 #pragma unroll
         for (int nb = 0; nb < C::NB; ++nb)
           mma<true>(c[nb], a[0], a[1], a[2], a[3], sg.q[nb][2 * i], sg.q[nb][2 * i + 1]);
@@ -459,7 +479,7 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
 #pragma unroll
       for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[blk][nb][j] = c[nb][j] * sg.f[nb][j & 1];
+        for (int j = 0; j < 4; ++j) s[blk][nb][j] = c[nb][j];
     } else {
       uint32_t ska[GW], skb[GW], bka[GW], bkb[GW];
       const uint32_t sa = sbase + (blk * 16 + row) * C::G * 2;
@@ -473,14 +493,14 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
         for (int j = 0; j < 4; ++j) s[blk][nb][j] = 0.0f;
       constexpr int SPAN = C::BITS == 4 ? 32 : 16;  // elements of four lanes' words
       constexpr int PER_GROUP = C::GS / SPAN;
-      const uint32_t ka = kb + row * C::RB + 4 * t;
+      const uint32_t ka = kb + row * C::RB + (sw << 4) + 4 * t;
 #pragma unroll
       for (int gr = 0; gr < C::G; ++gr) {
         float c[C::NB][4] = {};
 #pragma unroll
         for (int ii = 0; ii < PER_GROUP; ++ii) {
           const int i = gr * PER_GROUP + ii;
-          const uint32_t at = ka + ((i ^ sw) << 4);
+          const uint32_t at = chunk_at<C::CH>(ka, i);
           const uint32_t w0 = ld_s32(at), w1 = ld_s32(at + 8 * C::RB);
           if constexpr (C::BITS == 4) {
             uint32_t u[4], v[4];
@@ -508,10 +528,6 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
             s[blk][nb][j] = fmaf(j < 2 ? s0 : s1, c[nb][j],
                                  fmaf(j < 2 ? b0 : b1, sg.x[gr][nb][j & 1], s[blk][nb][j]));
       }
-#pragma unroll
-      for (int nb = 0; nb < C::NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[blk][nb][j] *= sg.f[nb][j & 1];
     }
   }
 
@@ -538,7 +554,7 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
 #pragma unroll
           for (int blk = 0; blk < C::TB; ++blk) {
             const int at = 16 * blk + row + 8 * (j >> 1);
-            if (t0 + at < k.n) to[at] = s[blk][nb][j];
+            if (t0 + at < k.n) to[at] = s[blk][nb][j] * sg.f[nb][j & 1];
           }
         }
       }
@@ -555,8 +571,8 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
       if constexpr (C::TB == 2) x = fmaxf(x, fmaxf(s[1][nb][i], s[1][nb][i + 2]));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      top[nb][i] = x;
-      raise |= x > sg.m[nb][i] + kLazy;
+      top[nb][i] = x * sg.f[nb][i];
+      raise |= top[nb][i] > sg.m[nb][i] + kLazy;
     }
   uint32_t sva[C::TB][GW], svb[C::TB][GW];
   float large = 0.0f;
@@ -614,7 +630,7 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
       for (int blk = 0; blk < C::TB; ++blk)
 #pragma unroll
         for (int j = i; j < 4; j += 2) {
-          s[blk][nb][j] = ex2(s[blk][nb][j] - m);
+          s[blk][nb][j] = ex2(fmaf(s[blk][nb][j], sg.f[nb][i], -m));
           sg.l[nb][i] += s[blk][nb][j];
         }
     }
@@ -631,11 +647,11 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
         b[nb][1] = movmatrix(pack16<true>(s[blk][nb][2], s[blk][nb][3]));
       }
       const int r = (lane & 7) + ((lane >> 4) << 3);
-      const uint32_t a0 = vb + r * C::RB;
+      const uint32_t a0 = vb + r * C::RB + ((((lane >> 3) & 1) ^ swizzle<C::CH>(lane & 7)) << 4);
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) {
         uint32_t a[4];
-        ldmatrix4<true>(a, a0 + (((2 * mt + ((lane >> 3) & 1)) ^ swizzle<C::CH>(lane & 7)) << 4));
+        ldmatrix4<true>(a, chunk_at<C::CH>(a0, 2 * mt));
 #pragma unroll
         for (int nb = 0; nb < C::NB; ++nb)
           mma<true>(sg.o[mt][nb], a[0], a[1], a[2], a[3], b[nb][0], b[nb][1]);
@@ -648,7 +664,9 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
       // the four slots of this lane's operand columns, and their rows
       const int ra = slot_of<C::CH>(2 * t), rb = slot_of<C::CH>(2 * t + 1);
       const int xa = swizzle<C::CH>(ra), xb = swizzle<C::CH>(rb);
-      const uint32_t va = vb + ra * C::RB, vc = vb + rb * C::RB;
+      const int w0 = C::VCH == 32 && C::BITS == 4 ? g & 3 : g;  // word of the first set
+      const uint32_t va = vb + ra * C::RB + (((w0 >> 2) ^ xa) << 4) + ((w0 & 3) << 2);
+      const uint32_t vc = vb + rb * C::RB + (((w0 >> 2) ^ xb) << 4) + ((w0 & 3) << 2);
 #pragma unroll
       for (int gr = 0; gr < C::G; ++gr) {
         uint32_t b[C::NB][2];
@@ -665,11 +683,10 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
 #pragma unroll
         for (int cc = 0; cc < C::GS / C::VCH; ++cc) {
           const int c = gr * (C::GS / C::VCH) + cc;
-          const int word = C::BITS == 8 ? 8 * c + g : C::VCH == 64 ? 8 * c + g : 4 * c + (g & 3);
-          const uint32_t oa = (((word >> 2) ^ xa) << 4) + ((word & 3) << 2);
-          const uint32_t ob = (((word >> 2) ^ xb) << 4) + ((word & 3) << 2);
-          const uint32_t w0 = ld_s32(va + oa), w1 = ld_s32(vc + ob);
-          const uint32_t w2 = ld_s32(va + oa + 8 * C::RB), w3 = ld_s32(vc + ob + 8 * C::RB);
+          const int chunk = c * (C::VCH == 32 && C::BITS == 4 ? 1 : 2);
+          const uint32_t aa = chunk_at<C::CH>(va, chunk), ab = chunk_at<C::CH>(vc, chunk);
+          const uint32_t w0 = ld_s32(aa), w1 = ld_s32(ab);
+          const uint32_t w2 = ld_s32(aa + 8 * C::RB), w3 = ld_s32(ab + 8 * C::RB);
           if constexpr (C::BITS == 8) {
             const uint32_t e0 = __byte_perm(w0, w1, 0x5140), e1 = __byte_perm(w0, w1, 0x7362);
             const uint32_t e2 = __byte_perm(w2, w3, 0x5140), e3 = __byte_perm(w2, w3, 0x7362);
@@ -708,44 +725,102 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
   }
 }
 
-// Fetches tiles ahead of the computation.
+// Fetches tiles ahead of the computation.  A 16-slot block lies in one page, so
+// its rows (and its scales of one kind) are contiguous: lane i copies their
+// 16-byte chunks i, i + 32, ...
 template <class C>
 struct Fetcher {
+  static constexpr int kCopies = (C::CH + 1) / 2;          // of a lane, for a block's keys
+  static constexpr int kScaleCopies = (8 * C::G + 31) / 32;
   Cursor k;
-  int page_at, in_page;        // page of the sequence, and 16-slot block within it
+  const int *entry;            // table entry of the next block's page
+  int in_page;                 // its place in the page, in blocks
+  int head_row;                // first row of the segment's head in a page
   int pages[C::TB];            // looked up one tile ahead
   int left;                    // tiles still to fetch
-  const uint16_t *scales[(8 * C::G + 31) / 32 ? (8 * C::G + 31) / 32 : 1];
+  uint32_t to, scale_to;       // this lane's first chunks in a stage
+  const uint8_t *keys, *values;
+  const uint16_t *scales[kScaleCopies ? kScaleCopies : 1];
 
   __device__ __forceinline__ void start(const AttnParams &p, const Cursor &at, int count, int lane) {
     k = at;
     left = count;
+    to = (lane / C::CH) * C::RB + (((lane % C::CH) ^ swizzle<C::CH>((lane / C::CH) & 7)) << 4);
+    keys = p.c.k + lane * 16;
+    values = p.c.v + lane * 16;
     if constexpr (C::BITS != 16) {
+      const int a0 = lane / (2 * C::G), j0 = lane - a0 * 2 * C::G;
+      scale_to = 2 * C::TILE * C::RB + a0 * C::TILE * C::G * 2 + j0 * 16;
 #pragma unroll
-      for (int i = 0; i < (8 * C::G + 31) / 32; ++i) {
-        const int a = (lane + 32 * i) / (2 * C::G);
-        scales[i] = a == 0 ? p.c.k_scales : a == 1 ? p.c.k_biases : a == 2 ? p.c.v_scales : p.c.v_biases;
+      for (int i = 0; i < kScaleCopies; ++i) {
+        const int a = (lane + 32 * i) / (2 * C::G), j = (lane + 32 * i) % (2 * C::G);
+        scales[i] = (a == 0 ? p.c.k_scales : a == 1 ? p.c.k_biases : a == 2 ? p.c.v_scales
+                                                                            : p.c.v_biases) + j * 8;
       }
     }
-    if (left > 0) place(p);
+    if (left > 0) segment(p);
   }
-  __device__ __forceinline__ void place(const AttnParams &p) {
-    const int blk = k.tile * C::TB, per = p.c.S / 16;
-    page_at = blk / per;
-    in_page = blk - page_at * per;
+  __device__ __forceinline__ void segment(const AttnParams &p) {
+    head_row = (p.chunks == 1 ? k.hc : k.hc / p.chunks) * p.c.S;
+    entry = p.c.table + static_cast<long long>(k.b) * p.c.width;
+    in_page = 0;
+    if (k.tile > 0) {
+      const int blk = k.tile * C::TB, per = p.c.S / 16;
+      entry += blk / per;
+      in_page = blk % per;
+    }
     look_up(p);
   }
+  // The next tile's pages; a block past the sequence's slots has none.
   __device__ __forceinline__ void look_up(const AttnParams &p) {
-    const int *row = p.c.table + static_cast<long long>(k.b) * p.c.width;
-    const int per = p.c.S / 16;
-    int at = page_at, in = in_page;
+    pages[0] = __ldg(entry);
+    if constexpr (C::TB == 2) {
+      pages[1] = pages[0];
+      if (in_page + 1 == p.c.S / 16)
+        pages[1] = k.tile * C::TILE + 16 < k.n ? __ldg(entry + 1) : -1;
+    }
+  }
+  // Copies one block's rows; `rows` of them are the sequence's, the others 0.
+  template <bool ALL>
+  __device__ __forceinline__ void copy_block(const AttnParams &p, int i, int page, int at, int rows,
+                                             uint32_t stage, int lane) {
+    const uint32_t first = static_cast<uint32_t>(page) * (p.c.H * p.c.S) + head_row + at;
+    const uint8_t *ks = keys + static_cast<unsigned long long>(first) * C::RB;
+    const uint8_t *vs = values + static_cast<unsigned long long>(first) * C::RB;
+    const uint32_t base = stage + to;
 #pragma unroll
-    for (int i = 0; i < C::TB; ++i) {
-      // a block past the sequence's slots is not looked up
-      pages[i] = k.tile * C::TILE + 16 * i < k.n ? __ldg(row + at) : -1;
-      if (++in == per) {
-        in = 0;
-        ++at;
+    for (int c = 0; c < kCopies; ++c) {
+      constexpr bool kEven = 32 % C::CH == 0;  // a copy is whole rows
+      constexpr int kRows = kEven ? 32 / C::CH : 1;
+      uint32_t dst;
+      int r;
+      if constexpr (kEven) {
+        r = lane / C::CH + c * kRows;
+        dst = (base ^ (swizzle<C::CH>((c * kRows) & 7) << 4)) + (16 * i + c * kRows) * C::RB;
+      } else {
+        r = (c * 32 + lane) / C::CH;
+        dst = stage + (16 * i + r) * C::RB + (((c * 32 + lane) % C::CH ^ swizzle<C::CH>(r & 7)) << 4);
+      }
+      if (C::CH % 2 == 0 || c * 32 + lane < 16 * C::CH) {
+        const int bytes = ALL || r < rows ? 16 : 0;
+        cp_async16(dst, ks + c * 512, bytes);
+        cp_async16(dst + C::TILE * C::RB, vs + c * 512, bytes);
+      }
+    }
+    if constexpr (C::BITS != 16) {
+#pragma unroll
+      for (int c = 0; c < kScaleCopies; ++c) {
+        if (8 * C::G % 32 == 0 || c * 32 + lane < 8 * C::G) {
+          const int j = (c * 32 + lane) % (2 * C::G);
+          int bytes = 16;
+          if (!ALL) {
+            bytes = rows * C::G * 2 - j * 16;
+            bytes = bytes < 0 ? 0 : bytes < 16 ? bytes : 16;
+          }
+          // the second copy's kinds (values) follow the first's (keys)
+          cp_async16(stage + scale_to + c * 2 * C::TILE * C::G * 2 + i * 32 * C::G,
+                     scales[c] + static_cast<unsigned long long>(first) * C::G, bytes);
+        }
       }
     }
   }
@@ -754,57 +829,40 @@ struct Fetcher {
                                             int lane) {
     uint32_t bad = 0u;
     if (left > 0) {
-      const int hk = k.hc / p.chunks, per = p.c.S / 16;
-      int in = in_page;
+      const int per = p.c.S / 16;
+      const int have = k.n - k.tile * C::TILE;
+      bool all = have >= C::TILE;
 #pragma unroll
-      for (int i = 0; i < C::TB; ++i) {
-        const int have = k.n - (k.tile * C::TILE + 16 * i);  // valid slots of the block
-        int page = pages[i];
-        int rows = have < 0 ? 0 : have < 16 ? have : 16;
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
-          if (rows > 0) {
-            bad |= 1u << i;
-            if (p.c.status && lane == 0) atomicOr(p.c.status, 1);
-          }
-          rows = 0;
-          page = 0;
-        }
-        const long long first = cache_row(p.c, page, hk, 16 * in);
-        const uint8_t *ks = p.c.k + first * C::RB + lane * 16, *vs = p.c.v + first * C::RB + lane * 16;
+      for (int i = 0; i < C::TB; ++i)
+        all &= static_cast<unsigned>(pages[i]) < static_cast<unsigned>(p.c.num_pages);
+      const int at1 = in_page + 1 == per ? 0 : in_page + 1;
+      if (all) {
 #pragma unroll
-        for (int c = 0; c < (C::CH + 1) / 2; ++c) {
-          const int ix = c * 32 + lane;
-          const int r = ix / C::CH, col = ix - r * C::CH;
-          if (C::CH % 2 == 0 || ix < 16 * C::CH) {
-            const uint32_t to = (16 * i + r) * C::RB + ((col ^ swizzle<C::CH>(r)) << 4);
-            const int bytes = r < rows ? 16 : 0;
-            cp_async16(stage + to, ks + c * 512, bytes);
-            cp_async16(stage + C::TILE * C::RB + to, vs + c * 512, bytes);
-          }
-        }
-        if constexpr (C::BITS != 16) {
+        for (int i = 0; i < C::TB; ++i)
+          copy_block<true>(p, i, pages[i], 16 * (i ? at1 : in_page), 16, stage, lane);
+      } else {
 #pragma unroll
-          for (int c = 0; c < (8 * C::G + 31) / 32; ++c) {
-            const int ix = c * 32 + lane;
-            if (ix < 8 * C::G) {
-              const int a = ix / (2 * C::G), j = ix - a * 2 * C::G;
-              int bytes = rows * C::G * 2 - j * 16;
-              bytes = bytes < 0 ? 0 : bytes < 16 ? bytes : 16;
-              cp_async16(stage + 2 * C::TILE * C::RB + a * C::TILE * C::G * 2 + i * 32 * C::G + j * 16,
-                         scales[c] + first * C::G + j * 8, bytes);
+        for (int i = 0; i < C::TB; ++i) {
+          int page = pages[i], rows = have - 16 * i;
+          rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
+          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
+            if (rows > 0) {
+              bad |= 1u << i;
+              if (p.c.status && lane == 0) atomicOr(p.c.status, 1);
             }
+            page = rows = 0;
           }
+          copy_block<false>(p, i, page, 16 * (i ? at1 : in_page), rows, stage, lane);
         }
-        if (++in == per) in = 0;
       }
       if (--left > 0) {
         if (cursor_next<C>(p, cum, k)) {
-          place(p);
+          segment(p);
         } else {
           in_page += C::TB;
           while (in_page >= per) {
             in_page -= per;
-            ++page_at;
+            ++entry;
           }
           look_up(p);
         }
@@ -1158,7 +1216,8 @@ cudaError_t attn_run(const AttnArgs &a, int sms) {
   p.Hq = a.num_q_heads;
   p.R = a.num_q_heads / a.cache.H;
   p.chunks = (p.R + C::HEADS - 1) / C::HEADS;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+  p.q_sign = a.scale < 0.0f ? 0x80008000u : 0u;
   p.weights = a.weights;
   p.state_width = a.state_width;
   p.room = static_cast<long long>(a.cache.width) * a.cache.S;
