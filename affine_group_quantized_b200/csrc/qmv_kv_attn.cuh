@@ -189,6 +189,9 @@ __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_fl
 __device__ __forceinline__ __half2 as_half2(uint32_t v) {
   return *reinterpret_cast<const __half2 *>(&v);
 }
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t v) {
+  return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+}
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t *>(&v); }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -215,6 +218,15 @@ __device__ __forceinline__ void nibbles(uint32_t x, uint32_t (&o)[4]) {
 template <int PAIR>
 __device__ __forceinline__ uint32_t bytes16(uint32_t x) {
   return __byte_perm(x, 0u, PAIR ? 0x4342 : 0x4140);
+}
+// Both nibbles' products of a byte come from the byte and its low nibble:
+// sum p (16 hi + lo) and sum p lo give sum p hi, which spares a mask.  Bytes 0
+// and 1 of x's 16-bit halves: o[0], o[2] the low nibbles, o[1], o[3] the bytes.
+__device__ __forceinline__ void nibble_bytes(uint32_t x, uint32_t (&o)[4]) {
+  o[1] = x & 0x00ff00ffu;
+  o[3] = __byte_perm(x, 0u, 0x4341);
+  o[0] = x & 0x000f000fu;
+  o[2] = o[3] & 0x000f000fu;
 }
 constexpr float kUnit = 5.9604644775390625e-8f;  // 2^-24
 
@@ -324,8 +336,14 @@ struct Segment {
   float o[C::MT][C::NB][4];
   float m[C::NB][2], l[C::NB][2];
   float pb[C::G ? C::G : 1][C::NB][2];               // sums of p * bias
-  float limit;                                       // largest scale for the current power
+  float allow[C::NB][2];                             // scores up to here leave m as it is
+  uint32_t limit;                                    // largest scale for vexp, a pair of bf16
   int vexp;                                          // values are scaled by 2^vexp
+
+  __device__ __forceinline__ void allow_scales(int e) {
+    vexp = e;
+    limit = (__float_as_uint(4096.0f * pow2(-e)) >> 16) * 0x10001u;  // a power of two
+  }
 
   __device__ __forceinline__ void start(const AttnParams &p, const Cursor &k, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -408,7 +426,7 @@ struct Segment {
         f[nb][0] = __shfl_sync(0xffffffffu, unit, 8 * t);
         f[nb][1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4);
       }
-      m[nb][0] = m[nb][1] = kNegInf;
+      m[nb][0] = m[nb][1] = allow[nb][0] = allow[nb][1] = kNegInf;
       l[nb][0] = l[nb][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::MT; ++i)
@@ -417,8 +435,7 @@ struct Segment {
 #pragma unroll
       for (int i = 0; i < C::G; ++i) pb[i][nb][0] = pb[i][nb][1] = 0.0f;
     }
-    vexp = 126;
-    limit = 4096.0f * pow2(-126);
+    allow_scales(126);
   }
 
   // The sums over all lanes of the warp: l, and the values in true units.
@@ -439,20 +456,27 @@ struct Segment {
 #pragma unroll
           for (int mt = 0; mt < C::MT; ++mt) {
             const int g = mt * 16 / C::GS;
-            // 2^24, or 2^20 where the codes were those of odd nibbles
-            const float unit = C::BITS == 4 && mt % 2 ? 0.0625f / kUnit : 1.0f / kUnit;
-            o[mt][nb][i] = fmaf(o[mt][nb][i] * unit, back, pb[g][nb][i]);
-            o[mt][nb][i + 2] = fmaf(o[mt][nb][i + 2] * unit, back, pb[g][nb][i]);
+            if (C::BITS == 4 && mt % 2 == 0) {  // the odd tile held 16 hi + lo
+              o[mt + 1][nb][i] = (o[mt + 1][nb][i] - o[mt][nb][i]) * 0.0625f;
+              o[mt + 1][nb][i + 2] = (o[mt + 1][nb][i + 2] - o[mt][nb][i + 2]) * 0.0625f;
+            }
+            o[mt][nb][i] = fmaf(o[mt][nb][i] * (1.0f / kUnit), back, pb[g][nb][i]);
+            o[mt][nb][i + 2] = fmaf(o[mt][nb][i + 2] * (1.0f / kUnit), back, pb[g][nb][i]);
           }
         }
       }
   }
 };
 
+// Whether a table entry names a page outside the cache.
+static __device__ __noinline__ bool outside(const int *entry, int num_pages) {
+  return static_cast<unsigned>(__ldg(entry)) >= static_cast<unsigned>(num_pages);
+}
+
 // One tile's scores, softmax step and value products.
 template <class C>
 __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p, const Cursor &k,
-                                            uint32_t stage, uint32_t bad, int lane) {
+                                            uint32_t stage, bool bad, int lane) {
   constexpr bool BF = C::BITS == 16;
   constexpr int GW = C::G ? (C::G + 1) / 2 : 1;
   const int g = lane >> 2, t = lane & 3;
@@ -531,16 +555,21 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
     }
   }
 
-  // slots past the sequence's, or of a bad page, take no part
+  // slots past the sequence's, or of a page outside the cache, take no part
   const int t0 = k.tile * C::TILE;
   if (bad || t0 + C::TILE > k.n) {
 #pragma unroll
-    for (int blk = 0; blk < C::TB; ++blk)
+    for (int blk = 0; blk < C::TB; ++blk) {
+      const int first = t0 + 16 * blk;
+      const bool off = bad && first < k.n &&
+                       outside(p.c.table + static_cast<long long>(k.b) * p.c.width + first / p.c.S,
+                               p.c.num_pages);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (((bad >> blk) & 1u) || t0 + 16 * blk + row + 8 * (j >> 1) >= k.n)
+        if (off || t0 + 16 * blk + row + 8 * (j >> 1) >= k.n)
 #pragma unroll
           for (int nb = 0; nb < C::NB; ++nb) s[blk][nb][j] = kNegInf;
+    }
   }
   if (p.scores) {
     const int hk = k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS;
@@ -560,7 +589,8 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
       }
   }
 
-  // running maximum, and the scales' power of two
+  // The running maximum is looked at lane by lane: only when some lane's slots
+  // exceed what it allows are the lanes' maxima brought together.
   float top[C::NB][2];
   bool raise = false;
 #pragma unroll
@@ -569,13 +599,11 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
     for (int i = 0; i < 2; ++i) {
       float x = fmaxf(s[0][nb][i], s[0][nb][i + 2]);
       if constexpr (C::TB == 2) x = fmaxf(x, fmaxf(s[1][nb][i], s[1][nb][i + 2]));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      top[nb][i] = x * sg.f[nb][i];
-      raise |= top[nb][i] > sg.m[nb][i] + kLazy;
+      top[nb][i] = x;
+      raise |= x > sg.allow[nb][i];
     }
   uint32_t sva[C::TB][GW], svb[C::TB][GW];
-  float large = 0.0f;
+  __nv_bfloat162 wide[GW];  // the largest scales, in pairs
   if constexpr (!BF) {
 #pragma unroll
     for (int blk = 0; blk < C::TB; ++blk) {
@@ -583,32 +611,40 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
       ld_groups<C::G>(a, sva[blk]);
       ld_groups<C::G>(a + 16 * C::G, svb[blk]);
 #pragma unroll
-      for (int gr = 0; gr < C::G; ++gr)
-        large = fmaxf(large, fmaxf(fabsf(group_value(sva[blk], gr)), fabsf(group_value(svb[blk], gr))));
+      for (int i = 0; i < GW; ++i) {
+        const __nv_bfloat162 m = __hmax2(__habs2(as_bf162(sva[blk][i])), __habs2(as_bf162(svb[blk][i])));
+        wide[i] = blk ? __hmax2(wide[i], m) : m;
+      }
     }
-    raise |= large > sg.limit;
+#pragma unroll
+    for (int i = 1; i < GW; ++i) wide[0] = __hmax2(wide[0], wide[i]);
+    raise |= !__hble2(wide[0], as_bf162(sg.limit));  // NaN scales do not count as small
   }
   if (__any_sync(0xffffffffu, raise)) {
     float ratio = 1.0f;
     if constexpr (!BF) {
+      float large = fmaxf(__low2float(wide[0]), __high2float(wide[0]));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) large = fmaxf(large, __shfl_xor_sync(0xffffffffu, large, o));
-      if (large > sg.limit) {
+      if (large > group_value(&sg.limit, 0)) {
         int e = 9 - (static_cast<int>(__float_as_uint(large) >> 23) - 127);
         e = e > 126 ? 126 : e < -118 ? -118 : e;
         const int step = e - sg.vexp;  // below 0
         ratio = step < -126 ? 0.0f : pow2(step);
-        sg.vexp = e;
-        sg.limit = 4096.0f * pow2(-e);
+        sg.allow_scales(e);
       }
     }
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float m = fmaxf(sg.m[nb][i], top[nb][i]);
+        float x = top[nb][i];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        const float m = fmaxf(sg.m[nb][i], x * sg.f[nb][i]);
         const float a = m == kNegInf ? 1.0f : ex2(sg.m[nb][i] - m);
         sg.m[nb][i] = m;
+        sg.allow[nb][i] = m == kNegInf ? kNegInf : (m + kLazy) / sg.f[nb][i];
         sg.l[nb][i] *= a;
 #pragma unroll
         for (int gr = 0; gr < C::G; ++gr) sg.pb[gr][nb][i] *= a;
@@ -699,10 +735,10 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
             }
           } else if constexpr (C::VCH == 64) {
             uint32_t u[4], v[4], y[4], z[4];
-            nibbles(__byte_perm(w0, w1, 0x5410), u);
-            nibbles(__byte_perm(w0, w1, 0x7632), v);
-            nibbles(__byte_perm(w2, w3, 0x5410), y);
-            nibbles(__byte_perm(w2, w3, 0x7632), z);
+            nibble_bytes(__byte_perm(w0, w1, 0x5410), u);
+            nibble_bytes(__byte_perm(w0, w1, 0x7632), v);
+            nibble_bytes(__byte_perm(w2, w3, 0x5410), y);
+            nibble_bytes(__byte_perm(w2, w3, 0x7632), z);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -711,8 +747,8 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
           } else {
             const uint32_t sel = g < 4 ? 0x5410u : 0x7632u;
             uint32_t u[4], y[4];
-            nibbles(__byte_perm(w0, w1, sel), u);
-            nibbles(__byte_perm(w2, w3, sel), y);
+            nibble_bytes(__byte_perm(w0, w1, sel), u);
+            nibble_bytes(__byte_perm(w2, w3, sel), y);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -738,6 +774,7 @@ struct Fetcher {
   int head_row;                // first row of the segment's head in a page
   int pages[C::TB];            // looked up one tile ahead
   int left;                    // tiles still to fetch
+  bool bad;                    // a page outside the cache was met
   uint32_t to, scale_to;       // this lane's first chunks in a stage
   const uint8_t *keys, *values;
   const uint16_t *scales[kScaleCopies ? kScaleCopies : 1];
@@ -745,6 +782,7 @@ struct Fetcher {
   __device__ __forceinline__ void start(const AttnParams &p, const Cursor &at, int count, int lane) {
     k = at;
     left = count;
+    bad = false;
     to = (lane / C::CH) * C::RB + (((lane % C::CH) ^ swizzle<C::CH>((lane / C::CH) & 7)) << 4);
     keys = p.c.k + lane * 16;
     values = p.c.v + lane * 16;
@@ -824,10 +862,9 @@ struct Fetcher {
       }
     }
   }
-  // Starts the copies of the next tile; returns the blocks of bad pages.
-  __device__ __forceinline__ uint32_t fetch(const AttnParams &p, const int *cum, uint32_t stage,
-                                            int lane) {
-    uint32_t bad = 0u;
+  // Starts the copies of the next tile.
+  __device__ __forceinline__ void fetch(const AttnParams &p, const int *cum, uint32_t stage,
+                                        int lane) {
     if (left > 0) {
       const int per = p.c.S / 16;
       const int have = k.n - k.tile * C::TILE;
@@ -847,7 +884,7 @@ struct Fetcher {
           rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
           if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
             if (rows > 0) {
-              bad |= 1u << i;
+              bad = true;
               if (p.c.status && lane == 0) atomicOr(p.c.status, 1);
             }
             page = rows = 0;
@@ -869,7 +906,6 @@ struct Fetcher {
       }
     }
     cp_commit();
-    return bad;
   }
 };
 
@@ -987,24 +1023,20 @@ attn_kernel(const AttnParams p) {
     Cursor k = cursor_at<C>(p, cum, u0);
     Fetcher<C> fetch;
     fetch.start(p, k, u1 - u0, lane);
-    uint32_t bad = 0u;  // TB bits for each stage of the ring
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i)
-      bad |= fetch.fetch(p, cum, ring + i * C::STAGE, lane) << (i * C::TB);
+    for (int i = 0; i < C::STAGES - 1; ++i) fetch.fetch(p, cum, ring + i * C::STAGE, lane);
     sg.start(p, k, lane);
-    int stage = 0, ahead = C::STAGES - 1, since = u0;  // first tile of the segment here
+    const uint32_t ring_end = ring + C::STAGES * C::STAGE;
+    uint32_t stage = ring, ahead = ring + (C::STAGES - 1) * C::STAGE;
+    int since = u0;  // first tile of the segment here
     for (int u = u0; u < u1; ++u) {
       cp_wait<C::STAGES - 2>();
       __syncwarp();
-      {
-        const uint32_t mask = (1u << C::TB) - 1u;
-        const uint32_t b = fetch.fetch(p, cum, ring + ahead * C::STAGE, lane);
-        bad = (bad & ~(mask << (ahead * C::TB))) | (b << (ahead * C::TB));
-        attend_tile<C>(sg, p, k, ring + stage * C::STAGE, (bad >> (stage * C::TB)) & mask, lane);
-      }
+      fetch.fetch(p, cum, ahead, lane);
+      attend_tile<C>(sg, p, k, stage, fetch.bad, lane);
       __syncwarp();
-      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-      ahead = ahead + 1 == C::STAGES ? 0 : ahead + 1;
+      ahead = stage;
+      stage = stage + C::STAGE == ring_end ? ring : stage + C::STAGE;
       const bool last = k.tile + 1 == k.tiles;
       if (last) {
         sg.finish();
