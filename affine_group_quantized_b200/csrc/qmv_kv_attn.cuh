@@ -271,18 +271,26 @@ __device__ __forceinline__ int clipped_length(const AttnParams &p, int b) {
   return len < 0 ? 0 : len < p.room ? len : static_cast<int>(p.room);
 }
 
-// The CTA whose warps hold tile u, when `total` tiles are shared out over
-// `warps` warps (warp i takes tiles [i * total / warps, (i + 1) * total / warps)).
-__device__ __forceinline__ int warp_of_tile(long long u, long long total, long long warps) {
-  return static_cast<int>(((u + 1) * warps - 1) / total);
-}
-
-// CTAs that take part: every one, or fewer where each warp would have less
-// than one tile.
-__device__ __forceinline__ int active_ctas(long long total, int ctas, int warps) {
-  const long long need = (total + warps - 1) / warps;
-  return static_cast<int>(need < ctas ? need : ctas);
-}
+// How `total` tiles are shared out over the warps of the CTAs that take part:
+// every CTA, or as many as leave no warp without a tile before the last.  Warp
+// i has `base` tiles, and one more where i < extra.
+struct Share {
+  int ctas, base, extra;
+  __device__ __forceinline__ Share(int total, int most, int warps) {
+    const int need = (total + warps - 1) / warps;
+    ctas = need < most ? need : most;
+    const int all = ctas * warps;
+    base = all ? total / all : 0;
+    extra = total - base * all;
+  }
+  __device__ __forceinline__ int first(int warp) const {
+    return warp * base + (warp < extra ? warp : extra);
+  }
+  __device__ __forceinline__ int warp_of(int tile) const {
+    const int bound = extra * (base + 1);
+    return tile < bound ? tile / (base + 1) : extra + (tile - bound) / base;
+  }
+};
 
 // Position in the numbered tiles.
 struct Cursor {
@@ -345,44 +353,48 @@ struct Segment {
     limit = (__float_as_uint(4096.0f * pow2(-e)) >> 16) * 0x10001u;  // a power of two
   }
 
-  __device__ __forceinline__ void start(const AttnParams &p, const Cursor &k, int lane) {
+  // elements of a lane's word, and words of a row that it has
+  static constexpr int PER = C::BITS == 16 ? 2 : 32 / C::BITS, STEPS = C::D / (4 * PER);
+
+  // The queries' bits, as they are (begin() makes operands of them): elements
+  // of word t + 4 i, or for bf16 rows the operands themselves.
+  __device__ __forceinline__ void load(const AttnParams &p, const Cursor &k, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const int hk = k.hc / p.chunks, ch = k.hc - hk * p.chunks;
-    // the same power of two for every group of sums below
+    const int hk = p.chunks == 1 ? k.hc : k.hc / p.chunks, ch = k.hc - hk * p.chunks;
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb) {
       const int r = ch * C::HEADS + nb * 8 + g;
       const bool live = r < p.R;
       const __nv_bfloat16 *row = p.q + k.b * p.q_stride + (hk * p.R + (live ? r : 0)) * C::D;
-      if constexpr (C::BITS == 16) {
 #pragma unroll
-        for (int i = 0; i < C::D / 16; ++i) {
-          const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * i + 2 * t);
-          q[nb][2 * i] = live ? __ldg(w) ^ p.q_sign : 0u;
-          q[nb][2 * i + 1] = live ? __ldg(w + 4) ^ p.q_sign : 0u;
+      for (int i = 0; i < STEPS; ++i) {
+        const __nv_bfloat16 *w = row + PER * (t + 4 * i);
+        if constexpr (C::BITS == 4) {
+          const uint4 v = live ? __ldg(reinterpret_cast<const uint4 *>(w)) : make_uint4(0, 0, 0, 0);
+          q[nb][4 * i] = v.x; q[nb][4 * i + 1] = v.y; q[nb][4 * i + 2] = v.z; q[nb][4 * i + 3] = v.w;
+        } else if constexpr (C::BITS == 8) {
+          const uint2 v = live ? __ldg(reinterpret_cast<const uint2 *>(w)) : make_uint2(0, 0);
+          q[nb][2 * i] = v.x; q[nb][2 * i + 1] = v.y;
+        } else {
+          q[nb][i] = live ? __ldg(reinterpret_cast<const uint32_t *>(w)) : 0u;
         }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void begin(const AttnParams &p, int lane) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int nb = 0; nb < C::NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < C::D / 8; ++i) q[nb][i] ^= p.q_sign;
+      if constexpr (C::BITS == 16) {
         f[nb][0] = f[nb][1] = p.scale_log2;
       } else {
-        // this lane's elements: of word t + 4 i, 8 (4-bit) or 4 (8-bit codes)
-        constexpr int PER = 32 / C::BITS, STEPS = C::D / (4 * PER);
-        uint32_t raw[STEPS][PER / 2];
         uint32_t top = 0u;
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          const __nv_bfloat16 *w = row + PER * (t + 4 * i);
-          if constexpr (PER == 8) {
-            const uint4 v = live ? __ldg(reinterpret_cast<const uint4 *>(w)) : make_uint4(0, 0, 0, 0);
-            raw[i][0] = v.x; raw[i][1] = v.y; raw[i][2] = v.z; raw[i][3] = v.w;
-          } else {
-            const uint2 v = live ? __ldg(reinterpret_cast<const uint2 *>(w)) : make_uint2(0, 0);
-            raw[i][0] = v.x; raw[i][1] = v.y;
-          }
-#pragma unroll
-          for (int j = 0; j < PER / 2; ++j) {
-            raw[i][j] ^= p.q_sign;
-            top = max(top, max(raw[i][j] & 0x7fffu, (raw[i][j] >> 16) & 0x7fffu));
-          }
-        }
+        for (int i = 0; i < C::D / 8; ++i)
+          top = max(top, max(q[nb][i] & 0x7fffu, (q[nb][i] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^e brings the largest to [2^14, 2^15); -114 <= e <= 126 keeps 2^e normal
@@ -397,8 +409,9 @@ struct Segment {
           float v[PER];
 #pragma unroll
           for (int j = 0; j < PER / 2; ++j) {
-            v[2 * j] = __uint_as_float(raw[i][j] << 16) * up;
-            v[2 * j + 1] = __uint_as_float(raw[i][j] & 0xffff0000u) * up;
+            const uint32_t raw = q[nb][PER / 2 * i + j];
+            v[2 * j] = __uint_as_float(raw << 16) * up;
+            v[2 * j + 1] = __uint_as_float(raw & 0xffff0000u) * up;
           }
           if constexpr (PER == 8) {
 #pragma unroll
@@ -809,6 +822,17 @@ struct Fetcher {
     }
     look_up(p);
   }
+  // Brings the queries of the segment closer: they are wanted a few tiles later.
+  __device__ __forceinline__ void call_queries(const AttnParams &p, int lane) {
+    constexpr int kLines = C::HEADS * C::D / 64;  // of 128 bytes
+    const int hk = p.chunks == 1 ? k.hc : k.hc / p.chunks;
+    const int r0 = hk * p.R + (k.hc - hk * p.chunks) * C::HEADS;
+    const __nv_bfloat16 *q = p.q + k.b * p.q_stride + r0 * C::D;
+#pragma unroll
+    for (int i = 0; i < kLines; i += 32)
+      if (lane + i < kLines && r0 + (lane + i) * 64 / C::D < p.Hq)
+        asm volatile("prefetch.global.L1 [%0];\n" ::"l"(q + (lane + i) * 64));
+  }
   // The next tile's pages; a block past the sequence's slots has none.
   __device__ __forceinline__ void look_up(const AttnParams &p) {
     pages[0] = __ldg(entry);
@@ -895,6 +919,7 @@ struct Fetcher {
       if (--left > 0) {
         if (cursor_next<C>(p, cum, k)) {
           segment(p);
+          call_queries(p, lane);
         } else {
           in_page += C::TB;
           while (in_page >= per) {
@@ -950,6 +975,13 @@ __device__ __forceinline__ void write_piece(const Segment<C> &sg, float *o, floa
     }
 }
 
+// Four elements of the output from their sums, divided by l.
+__device__ __forceinline__ void store_out(__nv_bfloat16 *to, float4 o, float l) {
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  *reinterpret_cast<uint2 *>(to) =
+      make_uint2(pack16<true>(o.x * inv, o.y * inv), pack16<true>(o.z * inv, o.w * inv));
+}
+
 // Tiles before every sequence, into shared memory (and the workspace, for the
 // second kernel).
 template <class C>
@@ -960,6 +992,29 @@ __device__ __forceinline__ void sum_tiles(const AttnParams &p, int *cum, int thr
   const int b0 = tid * per < p.batch ? tid * per : p.batch;
   const int b1 = b0 + per < p.batch ? b0 + per : p.batch;
   const int unit = p.c.H * p.chunks;
+  if (p.batch <= 32) {  // every warp for itself (all write the same), without a barrier
+    int mine = 0;
+    if (lane < p.batch) {
+      if (p.c.status && blockIdx.x == 0 && __ldg(p.lens + lane) > p.room) atomicOr(p.c.status, 1);
+      mine = (clipped_length(p, lane) + C::TILE - 1) / C::TILE * unit;
+    }
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane < p.batch) {
+      cum[lane + 1] = upto;
+      if (blockIdx.x == 0) p.cum[lane + 1] = upto;
+    }
+    if (lane == 0) {
+      cum[0] = 0;
+      if (blockIdx.x == 0) p.cum[0] = 0;
+    }
+    __syncwarp();
+    return;
+  }
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     if (p.c.status && blockIdx.x == 0 && __ldg(p.lens + b) > p.room) atomicOr(p.c.status, 1);
@@ -1006,14 +1061,12 @@ attn_kernel(const AttnParams p) {
       for (int i = tid; i < p.Hq * C::D / 8; i += C::WARPS * 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  const int ctas = active_ctas(total, p.ctas, C::WARPS);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const Share share(total, p.ctas, C::WARPS);
+  if (static_cast<int>(blockIdx.x) >= share.ctas) return;
 
-  const long long warps = static_cast<long long>(ctas) * C::WARPS;
-  const long long me = static_cast<long long>(blockIdx.x) * C::WARPS + warp;
-  const int u0 = static_cast<int>(me * total / warps), u1 = static_cast<int>((me + 1) * total / warps);
-  const int c0 = static_cast<int>((me - warp) * total / warps);
-  const int c1 = static_cast<int>((me - warp + C::WARPS) * total / warps);
+  const int cta_warp = blockIdx.x * C::WARPS, me = cta_warp + warp;
+  const int u0 = share.first(me), u1 = share.first(me + 1);
+  const int c0 = share.first(cta_warp), c1 = share.first(cta_warp + C::WARPS);
   const uint32_t ring = smem_addr(attn_smem) + warp * C::STAGES * C::STAGE;
   if (lane == 0) piece_seg[0][warp] = piece_seg[1][warp] = -1;
 
@@ -1021,11 +1074,12 @@ attn_kernel(const AttnParams p) {
   Segment<C> sg;
   if (u0 < u1) {
     Cursor k = cursor_at<C>(p, cum, u0);
+    sg.load(p, k, lane);
     Fetcher<C> fetch;
     fetch.start(p, k, u1 - u0, lane);
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) fetch.fetch(p, cum, ring + i * C::STAGE, lane);
-    sg.start(p, k, lane);
+    sg.begin(p, lane);
     const uint32_t ring_end = ring + C::STAGES * C::STAGE;
     uint32_t stage = ring, ahead = ring + (C::STAGES - 1) * C::STAGE;
     int since = u0;  // first tile of the segment here
@@ -1043,13 +1097,14 @@ attn_kernel(const AttnParams p) {
         if (u + 1 - k.tiles >= u0) {  // the whole segment was here
           write_out<C>(sg, p, k, lane);
         } else {
-          write_piece<C>(sg, p.warp_o + me * C::HEADS * C::D, piece_ml[0][warp], lane);
+          write_piece<C>(sg, p.warp_o + static_cast<long long>(me) * C::HEADS * C::D, piece_ml[0][warp], lane);
           if (lane == 0) piece_seg[0][warp] = k.b * unit + k.hc;
         }
         since = u + 1;
         if (u + 1 < u1) {
           cursor_next<C>(p, cum, k);
-          sg.start(p, k, lane);
+          sg.load(p, k, lane);
+          sg.begin(p, lane);
         }
       } else {
         ++k.tile;
@@ -1068,49 +1123,50 @@ attn_kernel(const AttnParams p) {
   if (tail) write_piece<C>(sg, tails + warp * C::HEADS * C::D, piece_ml[1][warp], lane);
   __syncthreads();
 
-  // join the pieces of a segment, in the order of its slots
-  for (int i = 0; i < 2 * C::WARPS;) {
-    const int seg = piece_seg[i & 1][i >> 1];
-    if (seg < 0) {
-      ++i;
-      continue;
-    }
-    int end = i + 1;
-    while (end < 2 * C::WARPS && (piece_seg[end & 1][end >> 1] == seg || piece_seg[end & 1][end >> 1] < 0)) ++end;
+  // Join the pieces of a segment, in the order of its slots: piece 2 w (+ 1) is
+  // warp w's first (last).  A thread has four neighbouring elements of a head.
+  const int mine = lane < 2 * C::WARPS ? piece_seg[lane & 1][lane >> 1] : -1;
+  unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
+  while (left) {
+    const int seg = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+    const unsigned run = __ballot_sync(0xffffffffu, mine == seg);
+    left &= ~run;
     const int b = seg / unit, hc = seg - b * unit;
     const int tiles = (cum[b + 1] - cum[b]) / unit;
     const int first = cum[b] + hc * tiles;
     const bool whole = first >= c0 && first + tiles <= c1;
-    const int slot = first < c0 ? 0 : 1;
     const int hk = hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
-    const long long part = (static_cast<long long>(blockIdx.x) * 2 + slot) * C::HEADS;
-    for (int e = tid; e < C::HEADS * C::D; e += C::WARPS * 32) {
+    const long long part = (static_cast<long long>(blockIdx.x) * 2 + (first < c0 ? 0 : 1)) * C::HEADS;
+    for (int e = 4 * tid; e < C::HEADS * C::D; e += 4 * C::WARPS * 32) {
       const int h = e / C::D, d = e - h * C::D;
       if (r0 + h >= p.R) break;
       float m = kNegInf;
-      for (int j = i; j < end; ++j)
-        if (piece_seg[j & 1][j >> 1] == seg) m = fmaxf(m, piece_ml[j & 1][j >> 1][h].x);
+      for (unsigned r = run; r; r &= r - 1) {
+        const int j = __ffs(r) - 1;
+        m = fmaxf(m, piece_ml[j & 1][j >> 1][h].x);
+      }
       const float ms = m == kNegInf ? 0.0f : m;
-      float l = 0.0f, o = 0.0f;
-      for (int j = i; j < end; ++j) {
-        if (piece_seg[j & 1][j >> 1] != seg) continue;
+      float l = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (unsigned r = run; r; r &= r - 1) {
+        const int j = __ffs(r) - 1;
         const float2 ml = piece_ml[j & 1][j >> 1][h];
         const float a = ex2(ml.x - ms);
         const float *from = (j & 1) ? tails + (j >> 1) * C::HEADS * C::D
-                                    : p.warp_o + (me - warp + (j >> 1)) * C::HEADS * C::D;
+                                    : p.warp_o + static_cast<long long>(cta_warp + (j >> 1)) * C::HEADS * C::D;
+        const float4 x = *reinterpret_cast<const float4 *>(from + e);
         l += a * ml.y;
-        o += a * from[e];
+        o.x += a * x.x; o.y += a * x.y; o.z += a * x.z; o.w += a * x.w;
       }
-      const long long head = static_cast<long long>(b) * p.Hq + hk * p.R + r0 + h;
       if (whole) {
-        p.out[head * C::D + d] = __float2bfloat16_rn(l > 0.0f ? o / l : 0.0f);
+        const long long head = static_cast<long long>(b) * p.Hq + hk * p.R + r0 + h;
+        store_out(p.out + head * C::D + d, o, l);
         if (p.scores && d == 0) p.stats[head] = make_float2(m, l);
       } else {
-        p.part_o[part * C::D + e] = o;
+        *reinterpret_cast<float4 *>(p.part_o + part * C::D + e) = o;
         if (d == 0) p.part_ml[part + h] = make_float2(m, l);
       }
     }
-    i = end;
   }
 }
 
@@ -1118,65 +1174,95 @@ attn_kernel(const AttnParams p) {
 // where no second step is needed.
 template <class C>
 __device__ __forceinline__ int2 segment_ctas(const AttnParams &p, int b, int hc) {
-  const int total = p.cum[p.batch], unit = p.c.H * p.chunks;
-  const int tiles = (p.cum[b + 1] - p.cum[b]) / unit;
-  const int first = p.cum[b] + hc * tiles;
-  const long long warps = static_cast<long long>(active_ctas(total, p.ctas, C::WARPS)) * C::WARPS;
-  return make_int2(warp_of_tile(first, total, warps) / C::WARPS,
-                   warp_of_tile(first + tiles - 1, total, warps) / C::WARPS);
+  const int total = __ldg(p.cum + p.batch), c0 = __ldg(p.cum + b), c1 = __ldg(p.cum + b + 1);
+  const int tiles = (c1 - c0) / (p.c.H * p.chunks);
+  const int first = c0 + hc * tiles;
+  const Share share(total, p.ctas, C::WARPS);
+  return make_int2(share.warp_of(first) / C::WARPS, share.warp_of(first + tiles - 1) / C::WARPS);
 }
 
 // Maximum and sum of one head over the CTAs that hold its segment.
 template <class C>
 __device__ __forceinline__ float2 joined_stats(const AttnParams &p, int2 at, int h) {
-  float m = kNegInf;
-  for (int c = at.x; c <= at.y; ++c)
-    m = fmaxf(m, p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h].x);
-  const float ms = m == kNegInf ? 0.0f : m;
-  float l = 0.0f;
+  float m = kNegInf, l = 0.0f;
   for (int c = at.x; c <= at.y; ++c) {
     const float2 ml = p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h];
-    l += ex2(ml.x - ms) * ml.y;
+    const float up = fmaxf(m, ml.x);
+    if (up != kNegInf) l = l * ex2(m - up) + ex2(ml.x - up) * ml.y;
+    m = up;
   }
   return make_float2(m, l);
 }
 
 constexpr int kWeightSlots = 1024;  // slots of a block that adds weights
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCtas = 32;       // pieces whose factors are kept at once
 
-// Second kernel: a block per (sequence, query head) joins what several CTAs
-// hold; further blocks add a kv head's probabilities into the weights.
+// Second kernel: a block per segment joins what several CTAs hold; further
+// blocks add a kv head's probabilities into the weights.
 template <class C>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int weight_blocks) {
   const int tid = threadIdx.x;
   wait_for_previous_grid();
-  const int heads = p.batch * p.Hq;
-  if (static_cast<int>(blockIdx.x) < heads) {
-    const int b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq;
-    if (p.cum[b + 1] == p.cum[b]) return;
-    const int hk = hq / p.R, r = hq - hk * p.R, ch = r / C::HEADS, h = r - ch * C::HEADS;
-    const int2 at = segment_ctas<C>(p, b, hk * p.chunks + ch);
+  const int unit = p.c.H * p.chunks, segments = p.batch * unit;
+  if (static_cast<int>(blockIdx.x) < segments) {
+    const int b = blockIdx.x / unit, hc = blockIdx.x - b * unit;
+    if (__ldg(p.cum + b + 1) == __ldg(p.cum + b)) return;
+    const int2 at = segment_ctas<C>(p, b, hc);
     if (at.x == at.y) return;
-    const float2 ml = joined_stats<C>(p, at, h);
-    const float ms = ml.x == kNegInf ? 0.0f : ml.x;
-    for (int d = tid; d < C::D; d += kJoinThreads) {
-      float o = 0.0f;
-      for (int c = at.x; c <= at.y; ++c) {
-        const long long i = (static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h;
-        o += ex2(p.part_ml[i].x - ms) * p.part_o[i * C::D + d];
+    const int hk = hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
+    constexpr int kOwn = (C::HEADS * C::D / 4 + kJoinThreads - 1) / kJoinThreads;
+    float4 o[kOwn] = {};
+    float l[kOwn] = {}, top[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) top[i] = kNegInf;
+    for (int c0 = at.x; c0 <= at.y; c0 += kJoinCtas) {
+      const int n = at.y + 1 - c0 < kJoinCtas ? at.y + 1 - c0 : kJoinCtas;
+      __shared__ float2 ml[kJoinCtas][C::HEADS];
+      __syncthreads();
+      for (int i = tid; i < n * C::HEADS; i += kJoinThreads) {
+        const int c = c0 + i / C::HEADS;
+        ml[i / C::HEADS][i % C::HEADS] =
+            p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + i % C::HEADS];
       }
-      p.out[static_cast<long long>(blockIdx.x) * C::D + d] =
-          __float2bfloat16_rn(ml.y > 0.0f ? o / ml.y : 0.0f);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int e = 4 * (tid + i * kJoinThreads);
+        if (e >= C::HEADS * C::D) break;
+        const int h = e / C::D;
+        float up = top[i];
+        for (int c = 0; c < n; ++c) up = fmaxf(up, ml[c][h].x);
+        if (up == kNegInf) continue;
+        const float a0 = ex2(top[i] - up);
+        top[i] = up;
+        l[i] *= a0;
+        o[i].x *= a0; o[i].y *= a0; o[i].z *= a0; o[i].w *= a0;
+#pragma unroll 8
+        for (int c = 0; c < n; ++c) {
+          const float a = ex2(ml[c][h].x - up);
+          const float4 x = *reinterpret_cast<const float4 *>(
+              p.part_o + ((static_cast<long long>(c0 + c) * 2 + (c0 + c == at.x)) * C::HEADS) * C::D + e);
+          l[i] += a * ml[c][h].y;
+          o[i].x += a * x.x; o[i].y += a * x.y; o[i].z += a * x.z; o[i].w += a * x.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int e = 4 * (tid + i * kJoinThreads), h = e / C::D;
+      if (e < C::HEADS * C::D && r0 + h < p.R)
+        store_out(p.out + (static_cast<long long>(b) * p.Hq + hk * p.R + r0) * C::D + e, o[i], l[i]);
     }
     return;
   }
-  const int ix = blockIdx.x - heads, row = ix / weight_blocks, z = ix - row * weight_blocks;
+  const int ix = blockIdx.x - segments, row = ix / weight_blocks, z = ix - row * weight_blocks;
   const int b = row / p.c.H, hk = row - b * p.c.H;
   const int n = clipped_length(p, b);
   const int j0 = z * kWeightSlots;
   if (j0 >= n) return;
   const int j1 = j0 + kWeightSlots < n ? j0 + kWeightSlots : n;
-  __shared__ float2 ml[64];
+  __shared__ float2 all[64];
   float sum[kWeightSlots / kJoinThreads] = {};
   for (int r0 = 0; r0 < p.R; r0 += 64) {
     const int count = p.R - r0 < 64 ? p.R - r0 : 64;
@@ -1184,12 +1270,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     if (tid < count) {
       const int r = r0 + tid, ch = r / C::HEADS;
       const int2 at = segment_ctas<C>(p, b, hk * p.chunks + ch);
-      ml[tid] = at.x == at.y ? p.stats[static_cast<long long>(b) * p.Hq + hk * p.R + r]
-                             : joined_stats<C>(p, at, r - ch * C::HEADS);
+      all[tid] = at.x == at.y ? p.stats[static_cast<long long>(b) * p.Hq + hk * p.R + r]
+                              : joined_stats<C>(p, at, r - ch * C::HEADS);
     }
     __syncthreads();
     for (int r = 0; r < count; ++r) {
-      const float m = ml[r].x, inv = 1.0f / ml[r].y;
+      const float m = all[r].x, inv = 1.0f / all[r].y;
       if (m == kNegInf) continue;  // no slot of the row takes part
       const float *s = p.scores + (static_cast<long long>(b) * p.Hq + hk * p.R + r0 + r) * p.room;
 #pragma unroll
@@ -1267,7 +1353,7 @@ cudaError_t attn_run(const AttnArgs &a, int sms) {
   if (e != cudaSuccess) return e;
   const int weight_blocks =
       a.weights ? static_cast<int>((p.room + kWeightSlots - 1) / kWeightSlots) : 0;
-  const long long blocks = static_cast<long long>(a.batch) * (p.Hq + static_cast<long long>(p.c.H) * weight_blocks);
+  const long long blocks = static_cast<long long>(a.batch) * p.c.H * (p.chunks + weight_blocks);
   return launch_overlapped(attn_join_kernel<C>, dim3(static_cast<unsigned>(blocks)), kJoinThreads, 0, 1,
                            a.stream, p, weight_blocks);
 }
