@@ -271,22 +271,26 @@ __device__ __forceinline__ int clipped_length(const AttnParams &p, int b) {
   return len < 0 ? 0 : len < p.room ? len : static_cast<int>(p.room);
 }
 
-// How `total` tiles are shared out over the warps of the CTAs that take part:
-// every CTA, or as many as leave no warp without a tile before the last.  Warp
-// i has `base` tiles, and one more where i < extra.
+// Fewest tiles of a CTA: with 8 a 2000-slot sequence of 8 kv heads took 11.5 us,
+// with 4, 2 and 1 (more CTAs to join) 12.5, 14.2 and 19.6 us; calls of a few
+// hundred slots did not differ.
+constexpr int kFew = 8;
+
+// How `total` tiles are shared out: over every CTA, or as many as have kFew
+// each.  CTA i has `base` tiles, and one more where i < extra; within it its
+// warps share them the same way.
 struct Share {
   int ctas, base, extra;
-  __device__ __forceinline__ Share(int total, int most, int warps) {
-    const int need = (total + warps - 1) / warps;
+  __device__ __forceinline__ Share(int total, int most) {
+    const int need = (total + kFew - 1) / kFew;
     ctas = need < most ? need : most;
-    const int all = ctas * warps;
-    base = all ? total / all : 0;
-    extra = total - base * all;
+    base = ctas ? total / ctas : 0;
+    extra = total - base * ctas;
   }
-  __device__ __forceinline__ int first(int warp) const {
-    return warp * base + (warp < extra ? warp : extra);
+  __device__ __forceinline__ int first(int cta) const {
+    return cta * base + (cta < extra ? cta : extra);
   }
-  __device__ __forceinline__ int warp_of(int tile) const {
+  __device__ __forceinline__ int cta_of(int tile) const {
     const int bound = extra * (base + 1);
     return tile < bound ? tile / (base + 1) : extra + (tile - bound) / base;
   }
@@ -303,13 +307,19 @@ __device__ __forceinline__ void cursor_sequence(const AttnParams &p, Cursor &k) 
   k.tiles = (k.n + C::TILE - 1) / C::TILE;
 }
 
+// `upto`: with at most 32 sequences, lane i's tiles up to and with sequence i.
 template <class C>
-__device__ __forceinline__ Cursor cursor_at(const AttnParams &p, const int *cum, int u) {
-  int lo = 0, hi = p.batch;  // cum[lo] <= u < cum[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= u) lo = mid;
-    else hi = mid;
+__device__ __forceinline__ Cursor cursor_at(const AttnParams &p, const int *cum, int upto, int u) {
+  int lo = 0;
+  if (p.batch <= 32) {
+    lo = __popc(__ballot_sync(0xffffffffu, upto <= u));
+  } else {
+    int hi = p.batch;  // cum[lo] <= u < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= u) lo = mid;
+      else hi = mid;
+    }
   }
   Cursor k;
   k.b = lo;
@@ -983,9 +993,9 @@ __device__ __forceinline__ void store_out(__nv_bfloat16 *to, float4 o, float l) 
 }
 
 // Tiles before every sequence, into shared memory (and the workspace, for the
-// second kernel).
+// second kernel).  Returns cursor_at's `upto`.
 template <class C>
-__device__ __forceinline__ void sum_tiles(const AttnParams &p, int *cum, int threads) {
+__device__ __forceinline__ int sum_tiles(const AttnParams &p, int *cum, int threads) {
   __shared__ int part[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + threads - 1) / threads;
@@ -1013,7 +1023,7 @@ __device__ __forceinline__ void sum_tiles(const AttnParams &p, int *cum, int thr
       if (blockIdx.x == 0) p.cum[0] = 0;
     }
     __syncwarp();
-    return;
+    return lane < p.batch ? upto : 0x7fffffff;
   }
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
@@ -1040,6 +1050,7 @@ __device__ __forceinline__ void sum_tiles(const AttnParams &p, int *cum, int thr
     if (blockIdx.x == 0) p.cum[p.batch] = before;
   }
   __syncthreads();
+  return 0;
 }
 
 template <class C>
@@ -1048,10 +1059,11 @@ attn_kernel(const AttnParams p) {
   extern __shared__ __align__(128) uint8_t attn_smem[];
   __shared__ float2 piece_ml[2][C::WARPS][C::HEADS];  // first and last pieces
   __shared__ int piece_seg[2][C::WARPS];              // segment, or -1
+  __shared__ int2 list[C::WARPS][2 * C::WARPS];       // pieces, for each warp: number, place
   int *cum = reinterpret_cast<int *>(attn_smem + C::SMEM);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_previous_grid();
-  sum_tiles<C>(p, cum, C::WARPS * 32);
+  const int upto = sum_tiles<C>(p, cum, C::WARPS * 32);
   const int total = cum[p.batch], unit = p.c.H * p.chunks;
 
   // rows of sequences without slots
@@ -1061,19 +1073,20 @@ attn_kernel(const AttnParams p) {
       for (int i = tid; i < p.Hq * C::D / 8; i += C::WARPS * 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  const Share share(total, p.ctas, C::WARPS);
+  const Share share(total, p.ctas);
   if (static_cast<int>(blockIdx.x) >= share.ctas) return;
 
   const int cta_warp = blockIdx.x * C::WARPS, me = cta_warp + warp;
-  const int u0 = share.first(me), u1 = share.first(me + 1);
-  const int c0 = share.first(cta_warp), c1 = share.first(cta_warp + C::WARPS);
+  const int c0 = share.first(blockIdx.x), c1 = share.first(blockIdx.x + 1);
+  const int each = (c1 - c0) / C::WARPS, more = (c1 - c0) % C::WARPS;
+  const int u0 = c0 + warp * each + (warp < more ? warp : more), u1 = u0 + each + (warp < more ? 1 : 0);
   const uint32_t ring = smem_addr(attn_smem) + warp * C::STAGES * C::STAGE;
   if (lane == 0) piece_seg[0][warp] = piece_seg[1][warp] = -1;
 
   bool tail = false;
   Segment<C> sg;
   if (u0 < u1) {
-    Cursor k = cursor_at<C>(p, cum, u0);
+    Cursor k = cursor_at<C>(p, cum, upto, u0);
     sg.load(p, k, lane);
     Fetcher<C> fetch;
     fetch.start(p, k, u1 - u0, lane);
@@ -1126,11 +1139,20 @@ attn_kernel(const AttnParams p) {
   // Join the pieces of a segment, in the order of its slots: piece 2 w (+ 1) is
   // warp w's first (last).  A thread has four neighbouring elements of a head.
   const int mine = lane < 2 * C::WARPS ? piece_seg[lane & 1][lane >> 1] : -1;
-  unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
-  while (left) {
+  const unsigned all = __ballot_sync(0xffffffffu, mine >= 0);
+  // each piece's place in the list, and its sums
+  if (mine >= 0) {
+    const int at = __popc(all & ((1u << lane) - 1u)), w = lane >> 1;
+    list[warp][at] = make_int2(lane, (lane & 1) ? w * C::HEADS * C::D : -1 - w);
+  }
+  __syncwarp();
+  unsigned left = all;
+  int i0 = 0, i1;
+  for (; left; i0 = i1) {
     const int seg = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
     const unsigned run = __ballot_sync(0xffffffffu, mine == seg);
     left &= ~run;
+    i1 = i0 + __popc(run);
     const int b = seg / unit, hc = seg - b * unit;
     const int tiles = (cum[b + 1] - cum[b]) / unit;
     const int first = cum[b] + hc * tiles;
@@ -1141,19 +1163,21 @@ attn_kernel(const AttnParams p) {
       const int h = e / C::D, d = e - h * C::D;
       if (r0 + h >= p.R) break;
       float m = kNegInf;
-      for (unsigned r = run; r; r &= r - 1) {
-        const int j = __ffs(r) - 1;
+#pragma unroll 4
+      for (int r = i0; r < i1; ++r) {
+        const int j = list[warp][r].x;
         m = fmaxf(m, piece_ml[j & 1][j >> 1][h].x);
       }
       const float ms = m == kNegInf ? 0.0f : m;
       float l = 0.0f;
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (unsigned r = run; r; r &= r - 1) {
-        const int j = __ffs(r) - 1;
-        const float2 ml = piece_ml[j & 1][j >> 1][h];
+#pragma unroll 4
+      for (int r = i0; r < i1; ++r) {
+        const int2 j = list[warp][r];
+        const float2 ml = piece_ml[j.x & 1][j.x >> 1][h];
         const float a = ex2(ml.x - ms);
-        const float *from = (j & 1) ? tails + (j >> 1) * C::HEADS * C::D
-                                    : p.warp_o + static_cast<long long>(cta_warp + (j >> 1)) * C::HEADS * C::D;
+        const float *from = j.y >= 0 ? tails + j.y
+                                     : p.warp_o + static_cast<long long>(cta_warp - 1 - j.y) * C::HEADS * C::D;
         const float4 x = *reinterpret_cast<const float4 *>(from + e);
         l += a * ml.y;
         o.x += a * x.x; o.y += a * x.y; o.z += a * x.z; o.w += a * x.w;
@@ -1177,8 +1201,8 @@ __device__ __forceinline__ int2 segment_ctas(const AttnParams &p, int b, int hc)
   const int total = __ldg(p.cum + p.batch), c0 = __ldg(p.cum + b), c1 = __ldg(p.cum + b + 1);
   const int tiles = (c1 - c0) / (p.c.H * p.chunks);
   const int first = c0 + hc * tiles;
-  const Share share(total, p.ctas, C::WARPS);
-  return make_int2(share.warp_of(first) / C::WARPS, share.warp_of(first + tiles - 1) / C::WARPS);
+  const Share share(total, p.ctas);
+  return make_int2(share.cta_of(first), share.cta_of(first + tiles - 1));
 }
 
 // Maximum and sum of one head over the CTAs that hold its segment.
