@@ -71,8 +71,8 @@ struct AttnParams {
   float *scores;       // [batch][Hq][room], with weights
   float2 *stats;       // [batch][Hq] maximum and sum of segments not joined by the second kernel
   float2 *part_ml;     // [ctas][2][heads]
-  float *part_o;       // [ctas][2][heads][D]
-  float *warp_o;       // [ctas][warps][heads][D]
+  float4 *part_o;      // [ctas][2] pieces of `quads` float4 (write_piece)
+  float4 *warp_o;      // [ctas][warps] pieces
   int ctas;
 };
 
@@ -98,11 +98,16 @@ struct AttnCfg {
   static constexpr int TILE = 16 * TB;
   static constexpr int STAGE = TILE * SLOT;
   static constexpr int RING = ROOM / STAGE;
-  static constexpr int STAGES = RING < 6 ? RING : 6;
+  // two tiles in flight, or 4 KB of them: 64 KB to an SM, where the latency of
+  // a copy times its share of the bandwidth is about 45 KB (more only made
+  // the start longer)
+  static constexpr int WANT = 2 + (4096 + STAGE - 1) / STAGE;
+  static constexpr int STAGES = RING < WANT ? RING : WANT;
   static_assert(STAGES >= 2, "a tile is fetched while another is computed");
   static constexpr int TAIL = HEADS * D * 4;           // a warp's last piece
   static constexpr int SMEM = WARPS * (STAGES * STAGE > TAIL ? STAGES * STAGE : TAIL);
   static constexpr int MT = D / 16;                    // 16-element accumulator tiles
+  static constexpr int QUADS = HEADS * D / 4;          // float4 of a piece
   // elements that one set of value words covers
   static constexpr int VCH = BITS == 4 && GS >= 64 ? 64 : 32;
 };
@@ -307,12 +312,16 @@ __device__ __forceinline__ void cursor_sequence(const AttnParams &p, Cursor &k) 
   k.tiles = (k.n + C::TILE - 1) / C::TILE;
 }
 
-// `upto`: with at most 32 sequences, lane i's tiles up to and with sequence i.
+// With at most 32 sequences, lane i knows sequence i: its slots, and the tiles
+// up to its end.
+struct Known {
+  int n, upto;
+};
 template <class C>
-__device__ __forceinline__ Cursor cursor_at(const AttnParams &p, const int *cum, int upto, int u) {
+__device__ __forceinline__ Cursor cursor_at(const AttnParams &p, const int *cum, Known known, int u) {
   int lo = 0;
   if (p.batch <= 32) {
-    lo = __popc(__ballot_sync(0xffffffffu, upto <= u));
+    lo = __popc(__ballot_sync(0xffffffffu, known.upto <= u));
   } else {
     int hi = p.batch;  // cum[lo] <= u < cum[hi]
     while (hi - lo > 1) {
@@ -323,7 +332,12 @@ __device__ __forceinline__ Cursor cursor_at(const AttnParams &p, const int *cum,
   }
   Cursor k;
   k.b = lo;
-  cursor_sequence<C>(p, k);
+  if (p.batch <= 32) {
+    k.n = __shfl_sync(0xffffffffu, known.n, lo);
+    k.tiles = (k.n + C::TILE - 1) / C::TILE;
+  } else {
+    cursor_sequence<C>(p, k);
+  }
   const int rest = u - cum[lo];
   k.hc = rest / k.tiles;
   k.tile = rest - k.hc * k.tiles;
@@ -944,12 +958,12 @@ struct Fetcher {
   }
 };
 
-// out of one head: bf16 values from sums and 1 / l
+// The output of a segment that was whole here.
 template <class C>
 __device__ __forceinline__ void write_out(const Segment<C> &sg, const AttnParams &p, const Cursor &k,
                                           int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int hk = k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS;
+  const int hk = p.chunks == 1 ? k.hc : k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS;
 #pragma unroll
   for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
@@ -959,43 +973,83 @@ __device__ __forceinline__ void write_out(const Segment<C> &sg, const AttnParams
       const long long head = static_cast<long long>(k.b) * p.Hq + hk * p.R + r;
       const float inv = sg.l[nb][i] > 0.0f ? 1.0f / sg.l[nb][i] : 0.0f;
       __nv_bfloat16 *to = p.out + head * C::D;
+      auto val = [&](int mt, int half) { return sg.o[mt][nb][i + 2 * half] * inv; };
+      if constexpr (C::BITS == 16) {
 #pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt) {
-        to[element_of<C>(mt, 0, g)] = __float2bfloat16_rn(sg.o[mt][nb][i] * inv);
-        to[element_of<C>(mt, 1, g)] = __float2bfloat16_rn(sg.o[mt][nb][i + 2] * inv);
+        for (int mt = 0; mt < C::MT; ++mt) {
+          to[element_of<C>(mt, 0, g)] = __float2bfloat16_rn(val(mt, 0));
+          to[element_of<C>(mt, 1, g)] = __float2bfloat16_rn(val(mt, 1));
+        }
+      } else if constexpr (C::VCH == 64) {  // 8 neighbours
+#pragma unroll
+        for (int mt = 0; mt < C::MT; mt += 4)
+          *reinterpret_cast<uint4 *>(to + element_of<C>(mt, 0, g)) =
+              make_uint4(pack16<true>(val(mt, 0), val(mt + 1, 0)), pack16<true>(val(mt + 2, 0), val(mt + 3, 0)),
+                         pack16<true>(val(mt, 1), val(mt + 1, 1)), pack16<true>(val(mt + 2, 1), val(mt + 3, 1)));
+      } else {  // 4
+#pragma unroll
+        for (int mt = 0; mt < C::MT; mt += 2)
+          *reinterpret_cast<uint2 *>(to + element_of<C>(mt, 0, g)) =
+              make_uint2(pack16<true>(val(mt, 0), val(mt + 1, 0)), pack16<true>(val(mt, 1), val(mt + 1, 1)));
       }
       if (p.scores && g == 0) p.stats[head] = make_float2(sg.m[nb][i], sg.l[nb][i]);
     }
 }
 
+// A piece of a segment: its accumulators as the lanes hold them (quad q of the
+// piece is accumulator tile q / 32, all lanes side by side), and its heads'
+// maxima and sums.
 template <class C>
-__device__ __forceinline__ void write_piece(const Segment<C> &sg, float *o, float2 *ml, int lane) {
+__device__ __forceinline__ void write_piece(const Segment<C> &sg, float4 *o, float2 *ml, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nb = 0; nb < C::NB; ++nb)
+  for (int nb = 0; nb < C::NB; ++nb) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int h = nb * 8 + 2 * t + i;
-#pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt) {
-        o[h * C::D + element_of<C>(mt, 0, g)] = sg.o[mt][nb][i];
-        o[h * C::D + element_of<C>(mt, 1, g)] = sg.o[mt][nb][i + 2];
-      }
-      if (g == 0) ml[h] = make_float2(sg.m[nb][i], sg.l[nb][i]);
+    for (int mt = 0; mt < C::MT; ++mt)
+      o[(mt * C::NB + nb) * 32 + lane] = make_float4(sg.o[mt][nb][0], sg.o[mt][nb][1], sg.o[mt][nb][2],
+                                                     sg.o[mt][nb][3]);
+    if (g == 0) {
+      ml[nb * 8 + 2 * t] = make_float2(sg.m[nb][0], sg.l[nb][0]);
+      ml[nb * 8 + 2 * t + 1] = make_float2(sg.m[nb][1], sg.l[nb][1]);
     }
+  }
 }
 
-// Four elements of the output from their sums, divided by l.
-__device__ __forceinline__ void store_out(__nv_bfloat16 *to, float4 o, float l) {
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  *reinterpret_cast<uint2 *>(to) =
-      make_uint2(pack16<true>(o.x * inv, o.y * inv), pack16<true>(o.z * inv, o.w * inv));
+// Quad q of a segment's output: two elements of two neighbouring heads, from
+// sums and the heads' l; `head0` is the segment's first head, `heads` how many
+// it has.
+template <class C>
+__device__ __forceinline__ void store_quad(__nv_bfloat16 *head0, int heads, int q, float4 o, float l0,
+                                           float l1) {
+  const int lane = q & 31, g = lane >> 2, tile = q >> 5, mt = tile / C::NB;
+  const int h = (tile % C::NB) * 8 + 2 * (lane & 3);
+  const float i0 = l0 > 0.0f ? 1.0f / l0 : 0.0f, i1 = l1 > 0.0f ? 1.0f / l1 : 0.0f;
+  __nv_bfloat16 *to = head0 + h * C::D;
+  const int a = element_of<C>(mt, 0, g), b = element_of<C>(mt, 1, g);
+  if (h < heads) {
+    to[a] = __float2bfloat16_rn(o.x * i0);
+    to[b] = __float2bfloat16_rn(o.z * i0);
+  }
+  if (h + 1 < heads) {
+    to[C::D + a] = __float2bfloat16_rn(o.y * i1);
+    to[C::D + b] = __float2bfloat16_rn(o.w * i1);
+  }
+}
+template <class C>
+__device__ __forceinline__ int quad_head(int q) {  // the first of its two heads
+  return (q >> 5) % C::NB * 8 + 2 * (q & 3);
+}
+__device__ __forceinline__ void add_quad(float4 &o, float2 a, const float4 &x) {
+  o.x = fmaf(a.x, x.x, o.x);
+  o.y = fmaf(a.y, x.y, o.y);
+  o.z = fmaf(a.x, x.z, o.z);
+  o.w = fmaf(a.y, x.w, o.w);
 }
 
 // Tiles before every sequence, into shared memory (and the workspace, for the
-// second kernel).  Returns cursor_at's `upto`.
+// second kernel).
 template <class C>
-__device__ __forceinline__ int sum_tiles(const AttnParams &p, int *cum, int threads) {
+__device__ __forceinline__ Known sum_tiles(const AttnParams &p, int *cum, int threads) {
   __shared__ int part[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + threads - 1) / threads;
@@ -1003,12 +1057,16 @@ __device__ __forceinline__ int sum_tiles(const AttnParams &p, int *cum, int thre
   const int b1 = b0 + per < p.batch ? b0 + per : p.batch;
   const int unit = p.c.H * p.chunks;
   if (p.batch <= 32) {  // every warp for itself (all write the same), without a barrier
-    int mine = 0;
+    int n = 0;
     if (lane < p.batch) {
-      if (p.c.status && blockIdx.x == 0 && __ldg(p.lens + lane) > p.room) atomicOr(p.c.status, 1);
-      mine = (clipped_length(p, lane) + C::TILE - 1) / C::TILE * unit;
+      n = __ldg(p.lens + lane);
+      if (n > p.room) {
+        n = static_cast<int>(p.room);
+        if (p.c.status && blockIdx.x == 0) atomicOr(p.c.status, 1);
+      }
+      n = n < 0 ? 0 : n;
     }
-    int upto = mine;
+    int upto = (n + C::TILE - 1) / C::TILE * unit;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -1023,7 +1081,7 @@ __device__ __forceinline__ int sum_tiles(const AttnParams &p, int *cum, int thre
       if (blockIdx.x == 0) p.cum[0] = 0;
     }
     __syncwarp();
-    return lane < p.batch ? upto : 0x7fffffff;
+    return {n, lane < p.batch ? upto : 0x7fffffff};
   }
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
@@ -1050,7 +1108,7 @@ __device__ __forceinline__ int sum_tiles(const AttnParams &p, int *cum, int thre
     if (blockIdx.x == 0) p.cum[p.batch] = before;
   }
   __syncthreads();
-  return 0;
+  return {0, 0};
 }
 
 template <class C>
@@ -1059,11 +1117,12 @@ attn_kernel(const AttnParams p) {
   extern __shared__ __align__(128) uint8_t attn_smem[];
   __shared__ float2 piece_ml[2][C::WARPS][C::HEADS];  // first and last pieces
   __shared__ int piece_seg[2][C::WARPS];              // segment, or -1
-  __shared__ int2 list[C::WARPS][2 * C::WARPS];       // pieces, for each warp: number, place
+  __shared__ __align__(8) float factor[2 * C::WARPS][C::HEADS];
+  __shared__ float2 joined[2 * C::WARPS][C::HEADS];   // maximum and sum of a piece's segment here
   int *cum = reinterpret_cast<int *>(attn_smem + C::SMEM);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_previous_grid();
-  const int upto = sum_tiles<C>(p, cum, C::WARPS * 32);
+  const Known known = sum_tiles<C>(p, cum, C::WARPS * 32);
   const int total = cum[p.batch], unit = p.c.H * p.chunks;
 
   // rows of sequences without slots
@@ -1086,7 +1145,7 @@ attn_kernel(const AttnParams p) {
   bool tail = false;
   Segment<C> sg;
   if (u0 < u1) {
-    Cursor k = cursor_at<C>(p, cum, upto, u0);
+    Cursor k = cursor_at<C>(p, cum, known, u0);
     sg.load(p, k, lane);
     Fetcher<C> fetch;
     fetch.start(p, k, u1 - u0, lane);
@@ -1110,7 +1169,7 @@ attn_kernel(const AttnParams p) {
         if (u + 1 - k.tiles >= u0) {  // the whole segment was here
           write_out<C>(sg, p, k, lane);
         } else {
-          write_piece<C>(sg, p.warp_o + static_cast<long long>(me) * C::HEADS * C::D, piece_ml[0][warp], lane);
+          write_piece<C>(sg, p.warp_o + static_cast<long long>(me) * C::QUADS, piece_ml[0][warp], lane);
           if (lane == 0) piece_seg[0][warp] = k.b * unit + k.hc;
         }
         since = u + 1;
@@ -1132,64 +1191,64 @@ attn_kernel(const AttnParams p) {
   }
   let_next_grid_start();
   __syncthreads();  // the rings are free
-  float *tails = reinterpret_cast<float *>(attn_smem);
-  if (tail) write_piece<C>(sg, tails + warp * C::HEADS * C::D, piece_ml[1][warp], lane);
+  float4 *tails = reinterpret_cast<float4 *>(attn_smem);
+  if (tail) write_piece<C>(sg, tails + warp * C::QUADS, piece_ml[1][warp], lane);
   __syncthreads();
 
   // Join the pieces of a segment, in the order of its slots: piece 2 w (+ 1) is
-  // warp w's first (last).  A thread has four neighbouring elements of a head.
+  // warp w's first (last).  First each piece's factor for each head ...
   const int mine = lane < 2 * C::WARPS ? piece_seg[lane & 1][lane >> 1] : -1;
   const unsigned all = __ballot_sync(0xffffffffu, mine >= 0);
-  // each piece's place in the list, and its sums
-  if (mine >= 0) {
-    const int at = __popc(all & ((1u << lane) - 1u)), w = lane >> 1;
-    list[warp][at] = make_int2(lane, (lane & 1) ? w * C::HEADS * C::D : -1 - w);
+  for (int i = tid; i < 2 * C::WARPS * C::HEADS; i += C::WARPS * 32) {
+    const int j = i / C::HEADS, h = i % C::HEADS, seg = piece_seg[j & 1][j >> 1];
+    if (seg < 0) continue;
+    float m = kNegInf, l = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 2 * C::WARPS; ++r)
+      if (piece_seg[r & 1][r >> 1] == seg) m = fmaxf(m, piece_ml[r & 1][r >> 1][h].x);
+    const float ms = m == kNegInf ? 0.0f : m;
+#pragma unroll
+    for (int r = 0; r < 2 * C::WARPS; ++r)
+      if (piece_seg[r & 1][r >> 1] == seg) {
+        const float2 ml = piece_ml[r & 1][r >> 1][h];
+        l += ex2(ml.x - ms) * ml.y;
+      }
+    factor[j][h] = ex2(piece_ml[j & 1][j >> 1][h].x - ms);
+    joined[j][h] = make_float2(m, l);
   }
-  __syncwarp();
-  unsigned left = all;
-  int i0 = 0, i1;
-  for (; left; i0 = i1) {
-    const int seg = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+  __syncthreads();
+  // ... then four sums a thread.
+  for (unsigned left = all; left;) {
+    const int j0 = __ffs(left) - 1;
+    const int seg = __shfl_sync(0xffffffffu, mine, j0);
     const unsigned run = __ballot_sync(0xffffffffu, mine == seg);
     left &= ~run;
-    i1 = i0 + __popc(run);
+    const int j1 = 31 - __clz(run);
     const int b = seg / unit, hc = seg - b * unit;
     const int tiles = (cum[b + 1] - cum[b]) / unit;
     const int first = cum[b] + hc * tiles;
-    const bool whole = first >= c0 && first + tiles <= c1;
     const int hk = hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
-    const long long part = (static_cast<long long>(blockIdx.x) * 2 + (first < c0 ? 0 : 1)) * C::HEADS;
-    for (int e = 4 * tid; e < C::HEADS * C::D; e += 4 * C::WARPS * 32) {
-      const int h = e / C::D, d = e - h * C::D;
-      if (r0 + h >= p.R) break;
-      float m = kNegInf;
-#pragma unroll 4
-      for (int r = i0; r < i1; ++r) {
-        const int j = list[warp][r].x;
-        m = fmaxf(m, piece_ml[j & 1][j >> 1][h].x);
-      }
-      const float ms = m == kNegInf ? 0.0f : m;
-      float l = 0.0f;
+    const long long part = static_cast<long long>(blockIdx.x) * 2 + (first < c0 ? 0 : 1);
+    const bool whole = first >= c0 && first + tiles <= c1;
+    const long long head = static_cast<long long>(b) * p.Hq + hk * p.R + r0;
+    for (int q = tid; q < C::QUADS; q += C::WARPS * 32) {
+      const int h = quad_head<C>(q);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-      for (int r = i0; r < i1; ++r) {
-        const int2 j = list[warp][r];
-        const float2 ml = piece_ml[j.x & 1][j.x >> 1][h];
-        const float a = ex2(ml.x - ms);
-        const float *from = j.y >= 0 ? tails + j.y
-                                     : p.warp_o + static_cast<long long>(cta_warp - 1 - j.y) * C::HEADS * C::D;
-        const float4 x = *reinterpret_cast<const float4 *>(from + e);
-        l += a * ml.y;
-        o.x += a * x.x; o.y += a * x.y; o.z += a * x.z; o.w += a * x.w;
+      for (int j = j0; j <= j1; ++j) {
+        if (!((run >> j) & 1u)) continue;
+        const float4 *from = (j & 1) ? tails + (j >> 1) * C::QUADS
+                                     : p.warp_o + static_cast<long long>(cta_warp + (j >> 1)) * C::QUADS;
+        add_quad(o, *reinterpret_cast<const float2 *>(&factor[j][h]), from[q]);
       }
-      if (whole) {
-        const long long head = static_cast<long long>(b) * p.Hq + hk * p.R + r0 + h;
-        store_out(p.out + head * C::D + d, o, l);
-        if (p.scores && d == 0) p.stats[head] = make_float2(m, l);
-      } else {
-        *reinterpret_cast<float4 *>(p.part_o + part * C::D + e) = o;
-        if (d == 0) p.part_ml[part + h] = make_float2(m, l);
-      }
+      if (whole)
+        store_quad<C>(p.out + head * C::D, p.R - r0, q, o, joined[j0][h].y, joined[j0][h + 1].y);
+      else
+        p.part_o[part * C::QUADS + q] = o;
+    }
+    if (tid < C::HEADS) {
+      if (!whole) p.part_ml[part * C::HEADS + tid] = joined[j0][tid];
+      else if (p.scores && r0 + tid < p.R) p.stats[head + tid] = joined[j0][tid];
     }
   }
 }
@@ -1235,48 +1294,53 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     const int2 at = segment_ctas<C>(p, b, hc);
     if (at.x == at.y) return;
     const int hk = hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
-    constexpr int kOwn = (C::HEADS * C::D / 4 + kJoinThreads - 1) / kJoinThreads;
+    constexpr int kOwn = (C::QUADS + kJoinThreads - 1) / kJoinThreads;
+    __shared__ float2 ml[kJoinCtas][C::HEADS];
+    __shared__ __align__(8) float factor[kJoinCtas][C::HEADS];
+    __shared__ __align__(8) float scale_by[C::HEADS], l[C::HEADS];
     float4 o[kOwn] = {};
-    float l[kOwn] = {}, top[kOwn];
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) top[i] = kNegInf;
+    float m = kNegInf, sum = 0.0f;  // of head `tid`
     for (int c0 = at.x; c0 <= at.y; c0 += kJoinCtas) {
       const int n = at.y + 1 - c0 < kJoinCtas ? at.y + 1 - c0 : kJoinCtas;
-      __shared__ float2 ml[kJoinCtas][C::HEADS];
+      // piece c0 + c is the CTA's second where the segment begins in it
+      auto piece = [&](int c) { return static_cast<long long>(c0 + c) * 2 + (c0 + c == at.x); };
+      for (int i = tid; i < n * C::HEADS; i += kJoinThreads)
+        ml[i / C::HEADS][i % C::HEADS] = p.part_ml[piece(i / C::HEADS) * C::HEADS + i % C::HEADS];
       __syncthreads();
-      for (int i = tid; i < n * C::HEADS; i += kJoinThreads) {
-        const int c = c0 + i / C::HEADS;
-        ml[i / C::HEADS][i % C::HEADS] =
-            p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + i % C::HEADS];
+      if (tid < C::HEADS) {
+        float up = m;
+        for (int c = 0; c < n; ++c) up = fmaxf(up, ml[c][tid].x);
+        const float us = up == kNegInf ? 0.0f : up;
+        const float a = ex2(m - us);
+        sum *= a;
+        for (int c = 0; c < n; ++c) {
+          const float f = ex2(ml[c][tid].x - us);
+          factor[c][tid] = f;
+          sum += f * ml[c][tid].y;
+        }
+        scale_by[tid] = a;
+        l[tid] = sum;
+        m = up;
       }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        const int e = 4 * (tid + i * kJoinThreads);
-        if (e >= C::HEADS * C::D) break;
-        const int h = e / C::D;
-        float up = top[i];
-        for (int c = 0; c < n; ++c) up = fmaxf(up, ml[c][h].x);
-        if (up == kNegInf) continue;
-        const float a0 = ex2(top[i] - up);
-        top[i] = up;
-        l[i] *= a0;
-        o[i].x *= a0; o[i].y *= a0; o[i].z *= a0; o[i].w *= a0;
+        const int q = tid + i * kJoinThreads;
+        if (q >= C::QUADS) break;
+        const int h = quad_head<C>(q);
+        const float2 a = *reinterpret_cast<const float2 *>(&scale_by[h]);
+        o[i].x *= a.x; o[i].y *= a.y; o[i].z *= a.x; o[i].w *= a.y;
 #pragma unroll 8
-        for (int c = 0; c < n; ++c) {
-          const float a = ex2(ml[c][h].x - up);
-          const float4 x = *reinterpret_cast<const float4 *>(
-              p.part_o + ((static_cast<long long>(c0 + c) * 2 + (c0 + c == at.x)) * C::HEADS) * C::D + e);
-          l[i] += a * ml[c][h].y;
-          o[i].x += a * x.x; o[i].y += a * x.y; o[i].z += a * x.z; o[i].w += a * x.w;
-        }
+        for (int c = 0; c < n; ++c)
+          add_quad(o[i], *reinterpret_cast<const float2 *>(&factor[c][h]), p.part_o[piece(c) * C::QUADS + q]);
       }
     }
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      const int e = 4 * (tid + i * kJoinThreads), h = e / C::D;
-      if (e < C::HEADS * C::D && r0 + h < p.R)
-        store_out(p.out + (static_cast<long long>(b) * p.Hq + hk * p.R + r0) * C::D + e, o[i], l[i]);
+      const int q = tid + i * kJoinThreads;
+      if (q < C::QUADS)
+        store_quad<C>(p.out + (static_cast<long long>(b) * p.Hq + hk * p.R + r0) * C::D, p.R - r0, q, o[i],
+                      l[quad_head<C>(q)], l[quad_head<C>(q) + 1]);
     }
     return;
   }
@@ -1337,8 +1401,8 @@ size_t lay_out(AttnParams &p, const CacheView &c, int batch, int num_q_heads, bo
   const size_t ctas = attn_ctas<C>(sms), heads = static_cast<size_t>(batch) * num_q_heads;
   p.cum = reinterpret_cast<int *>(take(4 * (static_cast<size_t>(batch) + 1)));
   p.part_ml = reinterpret_cast<float2 *>(take(ctas * 2 * C::HEADS * 8));
-  p.part_o = reinterpret_cast<float *>(take(ctas * 2 * C::HEADS * C::D * 4));
-  p.warp_o = reinterpret_cast<float *>(take(ctas * C::WARPS * C::HEADS * C::D * 4));
+  p.part_o = reinterpret_cast<float4 *>(take(ctas * 2 * C::HEADS * C::D * 4));
+  p.warp_o = reinterpret_cast<float4 *>(take(ctas * C::WARPS * C::HEADS * C::D * 4));
   if (weights) {
     p.stats = reinterpret_cast<float2 *>(take(heads * 8));
     p.scores = reinterpret_cast<float *>(take(heads * c.width * c.S * 4));
