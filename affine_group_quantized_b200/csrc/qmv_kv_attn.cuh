@@ -70,6 +70,7 @@ struct AttnParams {
   int *cum;            // [batch + 1] tiles before a sequence
   float *scores;       // [batch][Hq][room], with weights
   float2 *stats;       // [batch][Hq] maximum and sum of segments not joined by the second kernel
+  int2 *cuts;          // [ctas] segments whose later / first piece a CTA holds, or -1
   float2 *part_ml;     // [ctas][2][heads]
   float4 *part_o;      // [ctas][2] pieces of `quads` float4 (write_piece)
   float4 *warp_o;      // [ctas][warps] pieces
@@ -833,9 +834,10 @@ struct Fetcher {
                                                                             : p.c.v_biases) + j * 8;
       }
     }
-    if (left > 0) segment(p);
+    if (left > 0) segment(p, lane);
   }
-  __device__ __forceinline__ void segment(const AttnParams &p) {
+  __device__ __forceinline__ void segment(const AttnParams &p, int lane) {
+    call_queries(p, lane);
     head_row = (p.chunks == 1 ? k.hc : k.hc / p.chunks) * p.c.S;
     entry = p.c.table + static_cast<long long>(k.b) * p.c.width;
     in_page = 0;
@@ -942,8 +944,7 @@ struct Fetcher {
       }
       if (--left > 0) {
         if (cursor_next<C>(p, cum, k)) {
-          segment(p);
-          call_queries(p, lane);
+          segment(p, lane);
         } else {
           in_page += C::TB;
           while (in_page >= per) {
@@ -1133,7 +1134,10 @@ attn_kernel(const AttnParams p) {
     }
   }
   const Share share(total, p.ctas);
-  if (static_cast<int>(blockIdx.x) >= share.ctas) return;
+  if (static_cast<int>(blockIdx.x) >= share.ctas) {
+    if (tid == 0) p.cuts[blockIdx.x] = make_int2(-1, -1);
+    return;
+  }
 
   const int cta_warp = blockIdx.x * C::WARPS, me = cta_warp + warp;
   const int c0 = share.first(blockIdx.x), c1 = share.first(blockIdx.x + 1);
@@ -1142,50 +1146,53 @@ attn_kernel(const AttnParams p) {
   const uint32_t ring = smem_addr(attn_smem) + warp * C::STAGES * C::STAGE;
   if (lane == 0) piece_seg[0][warp] = piece_seg[1][warp] = -1;
 
+  // (The code of what follows runs once or twice in a warp, from a cold
+  // instruction cache: one copy of each part, in loops that are not unrolled.)
   bool tail = false;
   Segment<C> sg;
   if (u0 < u1) {
     Cursor k = cursor_at<C>(p, cum, known, u0);
-    sg.load(p, k, lane);
     Fetcher<C> fetch;
     fetch.start(p, k, u1 - u0, lane);
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) fetch.fetch(p, cum, ring + i * C::STAGE, lane);
-    sg.begin(p, lane);
     const uint32_t ring_end = ring + C::STAGES * C::STAGE;
-    uint32_t stage = ring, ahead = ring + (C::STAGES - 1) * C::STAGE;
-    int since = u0;  // first tile of the segment here
-    for (int u = u0; u < u1; ++u) {
-      cp_wait<C::STAGES - 2>();
-      __syncwarp();
+    uint32_t stage = ring, ahead = ring;
+    bool fresh = true;
+#pragma unroll 1
+    for (int u = u0 - (C::STAGES - 1); u < u1; ++u) {
+      if (u >= u0) {
+        cp_wait<C::STAGES - 2>();
+        __syncwarp();
+      }
       fetch.fetch(p, cum, ahead, lane);
+      ahead = ahead + C::STAGE == ring_end ? ring : ahead + C::STAGE;
+      if (u < u0) continue;
+      if (fresh) {
+        sg.load(p, k, lane);
+        sg.begin(p, lane);
+        fresh = false;
+      }
       attend_tile<C>(sg, p, k, stage, fetch.bad, lane);
       __syncwarp();
-      ahead = stage;
       stage = stage + C::STAGE == ring_end ? ring : stage + C::STAGE;
       const bool last = k.tile + 1 == k.tiles;
-      if (last) {
+      if (last || u + 1 == u1) {
         sg.finish();
+        if (!last) {  // the segment goes on in the next warp
+          tail = true;
+          if (lane == 0) piece_seg[1][warp] = k.b * unit + k.hc;
+          break;
+        }
         if (u + 1 - k.tiles >= u0) {  // the whole segment was here
           write_out<C>(sg, p, k, lane);
         } else {
           write_piece<C>(sg, p.warp_o + static_cast<long long>(me) * C::QUADS, piece_ml[0][warp], lane);
           if (lane == 0) piece_seg[0][warp] = k.b * unit + k.hc;
         }
-        since = u + 1;
-        if (u + 1 < u1) {
-          cursor_next<C>(p, cum, k);
-          sg.load(p, k, lane);
-          sg.begin(p, lane);
-        }
+        fresh = true;
+        if (u + 1 < u1) cursor_next<C>(p, cum, k);
       } else {
         ++k.tile;
       }
-    }
-    if (since < u1) {  // the segment goes on in the next warp
-      tail = true;
-      sg.finish();
-      if (lane == 0) piece_seg[1][warp] = k.b * unit + k.hc;
     }
     cp_wait<0>();
   }
@@ -1203,11 +1210,11 @@ attn_kernel(const AttnParams p) {
     const int j = i / C::HEADS, h = i % C::HEADS, seg = piece_seg[j & 1][j >> 1];
     if (seg < 0) continue;
     float m = kNegInf, l = 0.0f;
-#pragma unroll
+#pragma unroll 4
     for (int r = 0; r < 2 * C::WARPS; ++r)
       if (piece_seg[r & 1][r >> 1] == seg) m = fmaxf(m, piece_ml[r & 1][r >> 1][h].x);
     const float ms = m == kNegInf ? 0.0f : m;
-#pragma unroll
+#pragma unroll 4
     for (int r = 0; r < 2 * C::WARPS; ++r)
       if (piece_seg[r & 1][r >> 1] == seg) {
         const float2 ml = piece_ml[r & 1][r >> 1][h];
@@ -1218,6 +1225,7 @@ attn_kernel(const AttnParams p) {
   }
   __syncthreads();
   // ... then four sums a thread.
+  int cut0 = -1, cut1 = -1;
   for (unsigned left = all; left;) {
     const int j0 = __ffs(left) - 1;
     const int seg = __shfl_sync(0xffffffffu, mine, j0);
@@ -1231,6 +1239,10 @@ attn_kernel(const AttnParams p) {
     const long long part = static_cast<long long>(blockIdx.x) * 2 + (first < c0 ? 0 : 1);
     const bool whole = first >= c0 && first + tiles <= c1;
     const long long head = static_cast<long long>(b) * p.Hq + hk * p.R + r0;
+    if (tid == 0 && !whole) {
+      if (first < c0) cut0 = seg;
+      else cut1 = seg;
+    }
     for (int q = tid; q < C::QUADS; q += C::WARPS * 32) {
       const int h = quad_head<C>(q);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1251,6 +1263,8 @@ attn_kernel(const AttnParams p) {
       else if (p.scores && r0 + tid < p.R) p.stats[head + tid] = joined[j0][tid];
     }
   }
+  // the segments that this CTA holds a later and a first piece of
+  if (tid == 0) p.cuts[blockIdx.x] = make_int2(cut0, cut1);
 }
 
 // CTAs that hold pieces of segment hc of sequence b: first and last, the same
@@ -1281,29 +1295,44 @@ constexpr int kWeightSlots = 1024;  // slots of a block that adds weights
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 32;       // pieces whose factors are kept at once
 
-// Second kernel: a block per segment joins what several CTAs hold; further
-// blocks add a kv head's probabilities into the weights.
+// Second kernel: block i joins the segment that begins in CTA i and goes on in
+// the next ones, if there is one; further blocks add a kv head's probabilities
+// into the weights.
 template <class C>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams p, int weight_blocks) {
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   wait_for_previous_grid();
-  const int unit = p.c.H * p.chunks, segments = p.batch * unit;
-  if (static_cast<int>(blockIdx.x) < segments) {
-    const int b = blockIdx.x / unit, hc = blockIdx.x - b * unit;
-    if (__ldg(p.cum + b + 1) == __ldg(p.cum + b)) return;
-    const int2 at = segment_ctas<C>(p, b, hc);
-    if (at.x == at.y) return;
-    const int hk = hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
-    constexpr int kOwn = (C::QUADS + kJoinThreads - 1) / kJoinThreads;
+  if (static_cast<int>(blockIdx.x) < p.ctas) {
+    const int cta = blockIdx.x, unit = p.c.H * p.chunks;
+    const int seg = p.cuts[cta].y;
+    // the CTAs behind that hold more of it (a warp looks at 32 of them)
+    int pieces = 1;
+    for (bool more = true; more;) {
+      const int c = cta + pieces + lane;
+      const unsigned same = __ballot_sync(0xffffffffu, c < p.ctas && p.cuts[c].x == seg);
+      pieces += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+      more = same == 0xffffffffu;
+    }
+    if (seg < 0) return;
+    const int b = seg / unit, hc = seg - b * unit;
+    const int hk = p.chunks == 1 ? hc : hc / p.chunks, r0 = (hc - hk * p.chunks) * C::HEADS;
+    constexpr int kOwn = (C::QUADS + kJoinThreads - 1) / kJoinThreads, kAhead = 4;
     __shared__ float2 ml[kJoinCtas][C::HEADS];
     __shared__ __align__(8) float factor[kJoinCtas][C::HEADS];
     __shared__ __align__(8) float scale_by[C::HEADS], l[C::HEADS];
     float4 o[kOwn] = {};
     float m = kNegInf, sum = 0.0f;  // of head `tid`
-    for (int c0 = at.x; c0 <= at.y; c0 += kJoinCtas) {
-      const int n = at.y + 1 - c0 < kJoinCtas ? at.y + 1 - c0 : kJoinCtas;
-      // piece c0 + c is the CTA's second where the segment begins in it
-      auto piece = [&](int c) { return static_cast<long long>(c0 + c) * 2 + (c0 + c == at.x); };
+    for (int c0 = 0; c0 < pieces; c0 += kJoinCtas) {
+      const int n = pieces - c0 < kJoinCtas ? pieces - c0 : kJoinCtas;
+      // the first piece is its CTA's second
+      auto piece = [&](int c) { return static_cast<long long>(cta + c0 + c) * 2 + (c0 + c == 0); };
+      float4 x[kOwn][kAhead];  // the first pieces' sums, on their way meanwhile
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c)
+          if (c < n && tid + i * kJoinThreads < C::QUADS)
+            x[i][c] = p.part_o[piece(c) * C::QUADS + tid + i * kJoinThreads];
       for (int i = tid; i < n * C::HEADS; i += kJoinThreads)
         ml[i / C::HEADS][i % C::HEADS] = p.part_ml[piece(i / C::HEADS) * C::HEADS + i % C::HEADS];
       __syncthreads();
@@ -1330,8 +1359,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
         const int h = quad_head<C>(q);
         const float2 a = *reinterpret_cast<const float2 *>(&scale_by[h]);
         o[i].x *= a.x; o[i].y *= a.y; o[i].z *= a.x; o[i].w *= a.y;
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c)
+          if (c < n) add_quad(o[i], *reinterpret_cast<const float2 *>(&factor[c][h]), x[i][c]);
 #pragma unroll 8
-        for (int c = 0; c < n; ++c)
+        for (int c = kAhead; c < n; ++c)
           add_quad(o[i], *reinterpret_cast<const float2 *>(&factor[c][h]), p.part_o[piece(c) * C::QUADS + q]);
       }
     }
@@ -1344,7 +1376,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     }
     return;
   }
-  const int ix = blockIdx.x - segments, row = ix / weight_blocks, z = ix - row * weight_blocks;
+  const int ix = blockIdx.x - p.ctas, row = ix / weight_blocks, z = ix - row * weight_blocks;
   const int b = row / p.c.H, hk = row - b * p.c.H;
   const int n = clipped_length(p, b);
   const int j0 = z * kWeightSlots;
@@ -1400,6 +1432,7 @@ size_t lay_out(AttnParams &p, const CacheView &c, int batch, int num_q_heads, bo
   };
   const size_t ctas = attn_ctas<C>(sms), heads = static_cast<size_t>(batch) * num_q_heads;
   p.cum = reinterpret_cast<int *>(take(4 * (static_cast<size_t>(batch) + 1)));
+  p.cuts = reinterpret_cast<int2 *>(take(ctas * 8));
   p.part_ml = reinterpret_cast<float2 *>(take(ctas * 2 * C::HEADS * 8));
   p.part_o = reinterpret_cast<float4 *>(take(ctas * 2 * C::HEADS * C::D * 4));
   p.warp_o = reinterpret_cast<float4 *>(take(ctas * C::WARPS * C::HEADS * C::D * 4));
@@ -1441,7 +1474,7 @@ cudaError_t attn_run(const AttnArgs &a, int sms) {
   if (e != cudaSuccess) return e;
   const int weight_blocks =
       a.weights ? static_cast<int>((p.room + kWeightSlots - 1) / kWeightSlots) : 0;
-  const long long blocks = static_cast<long long>(a.batch) * p.c.H * (p.chunks + weight_blocks);
+  const long long blocks = p.ctas + static_cast<long long>(a.batch) * p.c.H * weight_blocks;
   return launch_overlapped(attn_join_kernel<C>, dim3(static_cast<unsigned>(blocks)), kJoinThreads, 0, 1,
                            a.stream, p, weight_blocks);
 }
