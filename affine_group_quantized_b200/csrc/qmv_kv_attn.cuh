@@ -61,6 +61,8 @@ struct AttnParams {
   __nv_bfloat16 *out;
   int batch, Hq, R;
   int chunks;          // segments of a kv head: ceil(R / heads of a segment)
+  int page_blocks;     // 16-slot blocks of a page
+  unsigned page_rows;  // rows of a page: kv heads * slots
   float scale_log2;    // |scale| * log2(e)
   uint32_t q_sign;     // flips the queries where scale is negative
   float *weights;      // or null
@@ -810,8 +812,9 @@ struct Fetcher {
   const int *entry;            // table entry of the next block's page
   int in_page;                 // its place in the page, in blocks
   int head_row;                // first row of the segment's head in a page
-  int pages[C::TB];            // looked up one tile ahead
+  int page, page1;             // that page, and the tile's second block's, looked up ahead
   int left;                    // tiles still to fetch
+  int full;                    // of which these, of the segment, have every slot
   bool bad;                    // a page outside the cache was met
   uint32_t to, scale_to;       // this lane's first chunks in a stage
   const uint8_t *keys, *values;
@@ -842,11 +845,21 @@ struct Fetcher {
     entry = p.c.table + static_cast<long long>(k.b) * p.c.width;
     in_page = 0;
     if (k.tile > 0) {
-      const int blk = k.tile * C::TB, per = p.c.S / 16;
-      entry += blk / per;
-      in_page = blk % per;
+      const int blk = k.tile * C::TB;
+      entry += blk / p.page_blocks;
+      in_page = blk % p.page_blocks;
     }
     look_up(p);
+    full = k.n / C::TILE - k.tile;
+  }
+  __device__ __forceinline__ void look_up(const AttnParams &p) {
+    page = __ldg(entry);
+    if constexpr (C::TB == 2) {
+      // the second block may begin the next page (a block past the slots has none)
+      page1 = in_page + 1 < p.page_blocks              ? page
+              : k.tile * C::TILE + 16 < k.n ? __ldg(entry + 1)
+                                            : -1;
+    }
   }
   // Brings the queries of the segment closer: they are wanted a few tiles later.
   __device__ __forceinline__ void call_queries(const AttnParams &p, int lane) {
@@ -859,100 +872,111 @@ struct Fetcher {
       if (lane + i < kLines && r0 + (lane + i) * 64 / C::D < p.Hq)
         asm volatile("prefetch.global.L1 [%0];\n" ::"l"(q + (lane + i) * 64));
   }
-  // The next tile's pages; a block past the sequence's slots has none.
-  __device__ __forceinline__ void look_up(const AttnParams &p) {
-    pages[0] = __ldg(entry);
-    if constexpr (C::TB == 2) {
-      pages[1] = pages[0];
-      if (in_page + 1 == p.c.S / 16)
-        pages[1] = k.tile * C::TILE + 16 < k.n ? __ldg(entry + 1) : -1;
-    }
-  }
-  // Copies one block's rows; `rows` of them are the sequence's, the others 0.
-  template <bool ALL>
-  __device__ __forceinline__ void copy_block(const AttnParams &p, int i, int page, int at, int rows,
-                                             uint32_t stage, int lane) {
-    const uint32_t first = static_cast<uint32_t>(page) * (p.c.H * p.c.S) + head_row + at;
+  // Copies BLOCKS blocks that follow one another in a page, from block `i` of
+  // the stage on; `rows` of their slots are the sequence's, the others 0.
+  template <bool ALL, int BLOCKS>
+  __device__ __forceinline__ void copy(const AttnParams &p, int i, int from, int at, int rows,
+                                       uint32_t stage, int lane) {
+    const uint32_t first = static_cast<uint32_t>(from) * p.page_rows + (head_row + at);
     const uint8_t *ks = keys + static_cast<unsigned long long>(first) * C::RB;
     const uint8_t *vs = values + static_cast<unsigned long long>(first) * C::RB;
     const uint32_t base = stage + to;
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) {
-      constexpr bool kEven = 32 % C::CH == 0;  // a copy is whole rows
-      constexpr int kRows = kEven ? 32 / C::CH : 1;
-      uint32_t dst;
-      int r;
-      if constexpr (kEven) {
-        r = lane / C::CH + c * kRows;
-        dst = (base ^ (swizzle<C::CH>((c * kRows) & 7) << 4)) + (16 * i + c * kRows) * C::RB;
-      } else {
-        r = (c * 32 + lane) / C::CH;
-        dst = stage + (16 * i + r) * C::RB + (((c * 32 + lane) % C::CH ^ swizzle<C::CH>(r & 7)) << 4);
+    for (int blk = 0; blk < BLOCKS; ++blk)
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        constexpr bool kEven = 32 % C::CH == 0;  // a copy is whole rows
+        constexpr int kRows = kEven ? 32 / C::CH : 1;
+        uint32_t dst;
+        int r;
+        if constexpr (kEven) {
+          r = lane / C::CH + c * kRows;
+          dst = (base ^ (swizzle<C::CH>((c * kRows) & 7) << 4)) + (16 * (i + blk) + c * kRows) * C::RB;
+        } else {
+          r = (c * 32 + lane) / C::CH;
+          dst = stage + (16 * (i + blk) + r) * C::RB +
+                (((c * 32 + lane) % C::CH ^ swizzle<C::CH>(r & 7)) << 4);
+        }
+        if (C::CH % 2 == 0 || c * 32 + lane < 16 * C::CH) {
+          const int bytes = ALL || 16 * blk + r < rows ? 16 : 0;
+          cp_async16(dst, ks + blk * 16 * C::RB + c * 512, bytes);
+          cp_async16(dst + C::TILE * C::RB, vs + blk * 16 * C::RB + c * 512, bytes);
+        }
       }
-      if (C::CH % 2 == 0 || c * 32 + lane < 16 * C::CH) {
-        const int bytes = ALL || r < rows ? 16 : 0;
-        cp_async16(dst, ks + c * 512, bytes);
-        cp_async16(dst + C::TILE * C::RB, vs + c * 512, bytes);
-      }
-    }
     if constexpr (C::BITS != 16) {
 #pragma unroll
       for (int c = 0; c < kScaleCopies; ++c) {
+        const uint16_t *ss = scales[c] + static_cast<unsigned long long>(first) * C::G;
         if (8 * C::G % 32 == 0 || c * 32 + lane < 8 * C::G) {
-          const int j = (c * 32 + lane) % (2 * C::G);
-          int bytes = 16;
-          if (!ALL) {
-            bytes = rows * C::G * 2 - j * 16;
-            bytes = bytes < 0 ? 0 : bytes < 16 ? bytes : 16;
+#pragma unroll
+          for (int blk = 0; blk < BLOCKS; ++blk) {
+            const int j = (c * 32 + lane) % (2 * C::G);
+            int bytes = 16;
+            if (!ALL) {
+              bytes = (rows - 16 * blk) * C::G * 2 - j * 16;
+              bytes = bytes < 0 ? 0 : bytes < 16 ? bytes : 16;
+            }
+            // the second copy's kinds (values) follow the first's (keys)
+            cp_async16(stage + scale_to + c * 2 * C::TILE * C::G * 2 + (i + blk) * 32 * C::G,
+                       ss + blk * 16 * C::G, bytes);
           }
-          // the second copy's kinds (values) follow the first's (keys)
-          cp_async16(stage + scale_to + c * 2 * C::TILE * C::G * 2 + i * 32 * C::G,
-                     scales[c] + static_cast<unsigned long long>(first) * C::G, bytes);
         }
       }
+    }
+  }
+  __device__ __forceinline__ bool inside(const AttnParams &p, int page) {
+    return static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
+  }
+  // A tile of fewer slots, or with a page outside the cache.
+  __device__ __forceinline__ void copy_partly(const AttnParams &p, uint32_t stage, int lane) {
+#pragma unroll 1
+    for (int i = 0; i < C::TB; ++i) {
+      int rows = k.n - k.tile * C::TILE - 16 * i, from = i ? page1 : page;
+      rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
+      if (!inside(p, from)) {
+        if (rows > 0) {
+          bad = true;
+          if (p.c.status && lane == 0) atomicOr(p.c.status, 1);
+        }
+        from = rows = 0;
+      }
+      copy<false, 1>(p, i, from, i && in_page + 1 == p.page_blocks ? 0 : 16 * (in_page + i), rows,
+                     stage, lane);
     }
   }
   // Starts the copies of the next tile.
   __device__ __forceinline__ void fetch(const AttnParams &p, const int *cum, uint32_t stage,
                                         int lane) {
     if (left > 0) {
-      const int per = p.c.S / 16;
-      const int have = k.n - k.tile * C::TILE;
-      bool all = have >= C::TILE;
-#pragma unroll
-      for (int i = 0; i < C::TB; ++i)
-        all &= static_cast<unsigned>(pages[i]) < static_cast<unsigned>(p.c.num_pages);
-      const int at1 = in_page + 1 == per ? 0 : in_page + 1;
-      if (all) {
-#pragma unroll
-        for (int i = 0; i < C::TB; ++i)
-          copy_block<true>(p, i, pages[i], 16 * (i ? at1 : in_page), 16, stage, lane);
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::TB; ++i) {
-          int page = pages[i], rows = have - 16 * i;
-          rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
-          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.c.num_pages)) {
-            if (rows > 0) {
-              bad = true;
-              if (p.c.status && lane == 0) atomicOr(p.c.status, 1);
-            }
-            page = rows = 0;
-          }
-          copy_block<false>(p, i, page, 16 * (i ? at1 : in_page), rows, stage, lane);
+      --left;
+      if (full > 0 && inside(p, page) && (C::TB == 1 || inside(p, page1))) {
+        if (in_page + C::TB <= p.page_blocks) {
+          copy<true, C::TB>(p, 0, page, 16 * in_page, 16 * C::TB, stage, lane);
+        } else {  // a page ends inside the tile
+          copy<true, 1>(p, 0, page, 16 * in_page, 16, stage, lane);
+          copy<true, 1>(p, 1, page1, 0, 16, stage, lane);
         }
+      } else {
+        copy_partly(p, stage, lane);
       }
-      if (--left > 0) {
-        if (cursor_next<C>(p, cum, k)) {
-          segment(p, lane);
-        } else {
-          in_page += C::TB;
-          while (in_page >= per) {
-            in_page -= per;
+      --full;
+      if (++k.tile < k.tiles) {
+        in_page += C::TB;
+        if (in_page >= p.page_blocks) {
+          in_page -= p.page_blocks;
+          ++entry;
+          if (C::TB > 1 && in_page >= p.page_blocks) {  // pages of one block
+            in_page -= p.page_blocks;
             ++entry;
           }
+          if (left > 0) look_up(p);
+        } else if (C::TB == 2 && in_page + 1 == p.page_blocks && left > 0) {
           look_up(p);
         }
+      } else if (left > 0) {
+        --k.tile;
+        cursor_next<C>(p, cum, k);
+        segment(p, lane);
       }
     }
     cp_commit();
@@ -1455,6 +1479,8 @@ cudaError_t attn_run(const AttnArgs &a, int sms) {
   p.Hq = a.num_q_heads;
   p.R = a.num_q_heads / a.cache.H;
   p.chunks = (p.R + C::HEADS - 1) / C::HEADS;
+  p.page_blocks = a.cache.S / 16;
+  p.page_rows = static_cast<unsigned>(a.cache.H) * a.cache.S;
   p.scale_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
   p.q_sign = a.scale < 0.0f ? 0x80008000u : 0u;
   p.weights = a.weights;
