@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqmv.so")
@@ -91,7 +92,9 @@ def lib() -> ctypes.CDLL:
                                    ctypes.c_size_t, P, P]
         L.kv_attention_workspace.argtypes = [C, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
         L.kv_evict.argtypes = [C] + [P] * 8 + [I] * 6 + [P, P]
-        for f in (L.kv_append, L.kv_read, L.kv_attention, L.kv_attention_workspace, L.kv_evict):
+        L.qmv_kv_words.argtypes = [I, I, ctypes.c_char_p]
+        for f in (L.kv_append, L.kv_read, L.kv_attention, L.kv_attention_workspace, L.kv_evict,
+                  L.qmv_kv_words):
             f.restype = I
         L.qmv_kv_last_error.restype = ctypes.c_char_p
         L.qmv_kv_last_error.argtypes = []
@@ -290,7 +293,7 @@ class KVCache:
         self.head_dim, self.bits, self.group_size = head_dim, bits, group_size
         self._struct = _KVCacheStruct(*(_ptr(t) for t in self.buffers), num_pages, num_kv_heads,
                                       page_size, head_dim, bits, group_size)
-        self._ref = ctypes.byref(self._struct)
+        self._address = ctypes.addressof(self._struct)
         self._device = _device_of(k)
 
 
@@ -303,46 +306,76 @@ def _device_of(t):
     return t.device.index
 
 
-def _same_device(cache, **tensors):
-    """Every tensor, and the current device, must be the cache's: a launch
-    goes to the current device."""
-    import torch
+def _on_device(cache):
+    """The current device must be the cache's: a launch goes to the current
+    device.  Returns the cache's device, or None for plain addresses."""
     want = cache._device
-    if want is None:
-        return
-    if torch.cuda.current_device() != want:
-        raise ValueError(f"the cache is on device {want}, the current device is "
-                         f"{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and not isinstance(t, int) and t.get_device() != want:
-            raise ValueError(f"{name}: not on the cache's device {want}")
+    if want is not None:
+        import torch
+        here = torch.cuda.current_device()
+        if here != want:
+            raise ValueError(f"the cache is on device {want}, the current device is {here}")
+    return want
 
 
-def _token_stride(name, t, stride, rows, heads, dim):
-    """The stride (elements) between the rows of a bf16 [rows, heads, dim]
-    argument, whose heads lie behind one another: a tensor's own, or the one
-    given (heads * dim when none is)."""
+def _arg(name, t, nbytes, size, device):
+    """The address of an argument of at least nbytes, contiguous, of `size`-byte
+    elements (None: any), on the cache's device."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name}: {t.nbytes} bytes, the call needs {nbytes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if size is not None and t.element_size() != size:
+        raise ValueError(f"{name}: must hold {size}-byte values")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name}: not on the cache's device {device}")
+    return t.data_ptr()
+
+
+def _arg_rows(name, t, stride, rows, heads, dim, device):
+    """Address and stride (elements) between the rows of a bf16 [rows, heads,
+    dim] argument whose heads lie behind one another: a tensor's own stride, or
+    the one given (heads * dim when none is)."""
     packed = heads * dim
     if t is None or isinstance(t, int):
-        return packed if stride is None else stride
-    if stride is None and t.dim() == 3 and tuple(t.shape) == (rows, heads, dim):
+        return t or 0, packed if stride is None else stride
+    if stride is None and t.dim() == 3 and t.shape == (rows, heads, dim):
         if t.element_size() != 2:
             raise ValueError(f"{name}: must hold bf16 values")
         s0, s1, s2 = t.stride()
         if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
             raise ValueError(f"{name}: a row's heads must be contiguous")
-        return s0 if rows > 1 else packed
+        if device is not None and t.get_device() != device:
+            raise ValueError(f"{name}: not on the cache's device {device}")
+        return t.data_ptr(), s0 if rows > 1 else packed
     stride = packed if stride is None else stride
-    _need(name, t, 2 * ((rows - 1) * stride + packed) if rows > 0 else 0)
-    return stride
+    need = 2 * ((rows - 1) * stride + packed) if rows > 0 else 0
+    return _arg(name, t, need, 2, device), stride
 
 
-def _need_int32(name, t, count):
-    if t is None or isinstance(t, int):
-        return
-    _need(name, t, 4 * count)
-    if t.element_size() != 4:
-        raise ValueError(f"{name}: must hold 4-byte values")
+def _kv_stream(stream, device):
+    """`stream`, or the current stream of the cache's device."""
+    if stream is None and device is not None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream) or 0
+
+
+# the calls of qmv_kv_words by number, and how their arguments are laid out
+_APPEND, _READ, _ATTENTION, _EVICT = range(4)
+_WORDS = (struct.Struct("17q"), struct.Struct("13q"), struct.Struct("16q"), struct.Struct("17q"))
+_FLOAT, _FLOAT_BITS = struct.Struct("f"), struct.Struct("i")
+_KV_NAMES = ("kv_append", "kv_read", "kv_attention", "kv_evict")
+
+
+def _kv_call(call, *words):
+    rc = lib().qmv_kv_words(call, len(words), _WORDS[call].pack(*words))
+    if rc != QMV_OK:
+        _check_kv(_KV_NAMES[call], rc)
 
 
 def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
@@ -352,24 +385,17 @@ def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, t
     tokens token_starts[b] .. token_starts[b+1]-1 (one token each without
     token_starts) fill its slots from lens[b] on (see include/qmv.h)."""
     H, D = cache.num_kv_heads, cache.head_dim
-    ks = _token_stride("k", k, k_stride, num_tokens, H, D)
-    vs = _token_stride("v", v, v_stride, num_tokens, H, D)
-    _kv_rows_need(block_table, lens, token_starts, batch, table_width)
-    _need_int32("seen", seen, batch)
-    _need_int32("positions", positions, batch * H * state_width)
-    _need_int32("weights", weights, batch * H * state_width)
-    _same_device(cache, k=k, v=v, block_table=block_table, lens=lens, token_starts=token_starts,
-                 seen=seen, positions=positions, weights=weights, d_status=d_status)
-    _check_kv("kv_append", lib().kv_append(
-        cache._ref, _ptr(k), _ptr(v), ks, vs, _ptr(block_table), _ptr(lens), _ptr(token_starts),
-        batch, num_tokens, table_width, _ptr(seen), _ptr(positions), _ptr(weights), state_width,
-        _ptr(d_status), _stream(stream)))
-
-
-def _kv_rows_need(block_table, lens, token_starts, batch, table_width):
-    _need_int32("block_table", block_table, batch * table_width)
-    _need_int32("lens", lens, batch)
-    _need_int32("token_starts", token_starts, batch + 1)
+    dev = _on_device(cache)
+    kp, ks = _arg_rows("k", k, k_stride, num_tokens, H, D, dev)
+    vp, vs = _arg_rows("v", v, v_stride, num_tokens, H, D, dev)
+    state = 4 * batch * H * state_width
+    _kv_call(_APPEND, cache._address, kp, vp, ks, vs,
+             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
+             _arg("lens", lens, 4 * batch, 4, dev),
+             _arg("token_starts", token_starts, 4 * batch + 4, 4, dev),
+             batch, num_tokens, table_width, _arg("seen", seen, 4 * batch, 4, dev),
+             _arg("positions", positions, state, 4, dev), _arg("weights", weights, state, 4, dev),
+             state_width, _arg("d_status", d_status, 4, 4, dev), _kv_stream(stream, dev))
 
 
 def kv_read(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
@@ -377,21 +403,23 @@ def kv_read(cache, k, v, block_table, lens, token_starts, batch, num_tokens, tab
     """Slots lens[b] .. of sequence b as dense bf16 rows token_starts[b] ..
     token_starts[b+1]-1 of k and v: the reverse of kv_append."""
     H, D = cache.num_kv_heads, cache.head_dim
-    ks = _token_stride("k", k, k_stride, num_tokens, H, D)
-    vs = _token_stride("v", v, v_stride, num_tokens, H, D)
-    _kv_rows_need(block_table, lens, token_starts, batch, table_width)
-    _same_device(cache, k=k, v=v, block_table=block_table, lens=lens, token_starts=token_starts,
-                 d_status=d_status)
-    _check_kv("kv_read", lib().kv_read(
-        cache._ref, _ptr(k), _ptr(v), ks, vs, _ptr(block_table), _ptr(lens), _ptr(token_starts),
-        batch, num_tokens, table_width, _ptr(d_status), _stream(stream)))
+    dev = _on_device(cache)
+    kp, ks = _arg_rows("k", k, k_stride, num_tokens, H, D, dev)
+    vp, vs = _arg_rows("v", v, v_stride, num_tokens, H, D, dev)
+    _kv_call(_READ, cache._address, kp, vp, ks, vs,
+             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
+             _arg("lens", lens, 4 * batch, 4, dev),
+             _arg("token_starts", token_starts, 4 * batch + 4, 4, dev),
+             batch, num_tokens, table_width, _arg("d_status", d_status, 4, 4, dev),
+             _kv_stream(stream, dev))
 
 
 def kv_attention_workspace(cache, batch, num_q_heads, table_width, with_weights=False) -> int:
     """Bytes of workspace kv_attention needs for these sizes, whatever the lengths."""
     n = ctypes.c_size_t(0)
     _check_kv("kv_attention_workspace", lib().kv_attention_workspace(
-        cache._ref, batch, num_q_heads, table_width, 1 if with_weights else 0, ctypes.byref(n)))
+        ctypes.byref(cache._struct), batch, num_q_heads, table_width, 1 if with_weights else 0,
+        ctypes.byref(n)))
     return n.value
 
 
@@ -401,21 +429,19 @@ def kv_attention(cache, q, block_table, lens, out, batch, num_q_heads, table_wid
     """Attention of one new token per sequence over its lens[b] slots; with
     weights, each slot's probabilities are added to them (see include/qmv.h).
     workspace: a tensor of kv_attention_workspace's bytes."""
-    D = cache.head_dim
-    qs = _token_stride("q", q, q_stride, batch, num_q_heads, D)
-    _need("out", out, 2 * batch * num_q_heads * D)
-    _need_int32("block_table", block_table, batch * table_width)
-    _need_int32("lens", lens, batch)
-    _need_int32("weights", weights, batch * cache.num_kv_heads * state_width)
-    _need("workspace", workspace, 0)
+    H, D = cache.num_kv_heads, cache.head_dim
     if workspace is None or isinstance(workspace, int):
         raise ValueError("workspace: must be a tensor")
-    _same_device(cache, q=q, block_table=block_table, lens=lens, out=out, weights=weights,
-                 workspace=workspace, d_status=d_status)
-    _check_kv("kv_attention", lib().kv_attention(
-        cache._ref, _ptr(q), qs, _ptr(block_table), _ptr(lens), _ptr(out), batch, num_q_heads,
-        table_width, scale, _ptr(weights), state_width, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(d_status), _stream(stream)))
+    dev = _on_device(cache)
+    qp, qs = _arg_rows("q", q, q_stride, batch, num_q_heads, D, dev)
+    _kv_call(_ATTENTION, cache._address, qp, qs,
+             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
+             _arg("lens", lens, 4 * batch, 4, dev),
+             _arg("out", out, 2 * batch * num_q_heads * D, 2, dev),
+             batch, num_q_heads, table_width, _FLOAT_BITS.unpack(_FLOAT.pack(scale))[0],
+             _arg("weights", weights, 4 * batch * H * state_width, 4, dev), state_width,
+             _arg("workspace", workspace, 0, None, dev), workspace.nbytes,
+             _arg("d_status", d_status, 4, 4, dev), _kv_stream(stream, dev))
 
 
 def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_weights,
@@ -424,17 +450,15 @@ def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_w
     """Keep the `budget` slots of every (sequence, kv head) with the largest
     weights, the newest `recent` and first `sinks` positions before all
     others, and move them below budget (see include/qmv.h)."""
-    state = batch * cache.num_kv_heads * state_width
-    for name, t, n in (("block_table", block_table, batch * table_width), ("lens", lens, batch),
-                       ("seen", seen, batch), ("weights", weights, state),
-                       ("positions", positions, state), ("new_lens", new_lens, batch),
-                       ("new_weights", new_weights, state),
-                       ("new_positions", new_positions, state)):
-        _need_int32(name, t, n)
-    _same_device(cache, block_table=block_table, lens=lens, seen=seen, weights=weights,
-                 positions=positions, new_lens=new_lens, new_weights=new_weights,
-                 new_positions=new_positions, d_status=d_status)
-    _check_kv("kv_evict", lib().kv_evict(
-        cache._ref, _ptr(block_table), _ptr(lens), _ptr(seen), _ptr(weights), _ptr(positions),
-        _ptr(new_lens), _ptr(new_weights), _ptr(new_positions), batch, table_width, state_width,
-        budget, recent, sinks, _ptr(d_status), _stream(stream)))
+    dev = _on_device(cache)
+    state = 4 * batch * cache.num_kv_heads * state_width
+    _kv_call(_EVICT, cache._address,
+             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
+             _arg("lens", lens, 4 * batch, 4, dev), _arg("seen", seen, 4 * batch, 4, dev),
+             _arg("weights", weights, state, 4, dev),
+             _arg("positions", positions, state, 4, dev),
+             _arg("new_lens", new_lens, 4 * batch, 4, dev),
+             _arg("new_weights", new_weights, state, 4, dev),
+             _arg("new_positions", new_positions, state, 4, dev),
+             batch, table_width, state_width, budget, recent, sinks,
+             _arg("d_status", d_status, 4, 4, dev), _kv_stream(stream, dev))

@@ -638,7 +638,8 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x = fmaxf(s[0][nb][i], s[0][nb][i + 2]);
-      if constexpr (C::TB == 2) x = fmaxf(x, fmaxf(s[1][nb][i], s[1][nb][i + 2]));
+#pragma unroll
+      for (int blk = 1; blk < C::TB; ++blk) x = fmaxf(x, fmaxf(s[blk][nb][i], s[blk][nb][i + 2]));
       top[nb][i] = x;
       raise |= x > sg.allow[nb][i];
     }
@@ -812,7 +813,7 @@ struct Fetcher {
   const int *entry;            // table entry of the next block's page
   int in_page;                 // its place in the page, in blocks
   int head_row;                // first row of the segment's head in a page
-  int page, page1;             // that page, and the tile's second block's, looked up ahead
+  int pages[C::TB];            // the pages of the next tile's blocks, looked up ahead
   int left;                    // tiles still to fetch
   int full;                    // of which these, of the segment, have every slot
   bool bad;                    // a page outside the cache was met
@@ -852,13 +853,19 @@ struct Fetcher {
     look_up(p);
     full = k.n / C::TILE - k.tile;
   }
+  // A block past the sequence's slots has no page.
   __device__ __forceinline__ void look_up(const AttnParams &p) {
-    page = __ldg(entry);
-    if constexpr (C::TB == 2) {
-      // the second block may begin the next page (a block past the slots has none)
-      page1 = in_page + 1 < p.page_blocks              ? page
-              : k.tile * C::TILE + 16 < k.n ? __ldg(entry + 1)
-                                            : -1;
+    pages[0] = __ldg(entry);
+    int in = in_page;
+    const int *e = entry;
+#pragma unroll
+    for (int i = 1; i < C::TB; ++i) {
+      pages[i] = pages[i - 1];
+      if (++in == p.page_blocks) {
+        in = 0;
+        ++e;
+        pages[i] = k.tile * C::TILE + 16 * i < k.n ? __ldg(e) : -1;
+      }
     }
   }
   // Brings the queries of the segment closer: they are wanted a few tiles later.
@@ -927,11 +934,12 @@ struct Fetcher {
   __device__ __forceinline__ bool inside(const AttnParams &p, int page) {
     return static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages);
   }
-  // A tile of fewer slots, or with a page outside the cache.
-  __device__ __forceinline__ void copy_partly(const AttnParams &p, uint32_t stage, int lane) {
-#pragma unroll 1
+  // A tile of fewer slots, or of several pages, or with a page outside the cache.
+  __device__ __forceinline__ void copy_apart(const AttnParams &p, uint32_t stage, int lane) {
+    int in = in_page;
+#pragma unroll
     for (int i = 0; i < C::TB; ++i) {
-      int rows = k.n - k.tile * C::TILE - 16 * i, from = i ? page1 : page;
+      int rows = k.n - k.tile * C::TILE - 16 * i, from = pages[i];
       rows = rows < 0 ? 0 : rows < 16 ? rows : 16;
       if (!inside(p, from)) {
         if (rows > 0) {
@@ -940,8 +948,8 @@ struct Fetcher {
         }
         from = rows = 0;
       }
-      copy<false, 1>(p, i, from, i && in_page + 1 == p.page_blocks ? 0 : 16 * (in_page + i), rows,
-                     stage, lane);
+      copy<false, 1>(p, i, from, 16 * in, rows, stage, lane);
+      if (++in == p.page_blocks) in = 0;
     }
   }
   // Starts the copies of the next tile.
@@ -949,30 +957,19 @@ struct Fetcher {
                                         int lane) {
     if (left > 0) {
       --left;
-      if (full > 0 && inside(p, page) && (C::TB == 1 || inside(p, page1))) {
-        if (in_page + C::TB <= p.page_blocks) {
-          copy<true, C::TB>(p, 0, page, 16 * in_page, 16 * C::TB, stage, lane);
-        } else {  // a page ends inside the tile
-          copy<true, 1>(p, 0, page, 16 * in_page, 16, stage, lane);
-          copy<true, 1>(p, 1, page1, 0, 16, stage, lane);
-        }
-      } else {
-        copy_partly(p, stage, lane);
-      }
+      if (full > 0 && in_page + C::TB <= p.page_blocks && inside(p, pages[0]))
+        copy<true, C::TB>(p, 0, pages[0], 16 * in_page, 16 * C::TB, stage, lane);
+      else
+        copy_apart(p, stage, lane);
       --full;
       if (++k.tile < k.tiles) {
+        const int *old = entry;
         in_page += C::TB;
-        if (in_page >= p.page_blocks) {
+        while (in_page >= p.page_blocks) {
           in_page -= p.page_blocks;
           ++entry;
-          if (C::TB > 1 && in_page >= p.page_blocks) {  // pages of one block
-            in_page -= p.page_blocks;
-            ++entry;
-          }
-          if (left > 0) look_up(p);
-        } else if (C::TB == 2 && in_page + 1 == p.page_blocks && left > 0) {
-          look_up(p);
         }
+        if (left > 0 && (entry != old || in_page + C::TB > p.page_blocks)) look_up(p);
       } else if (left > 0) {
         --k.tile;
         cursor_next<C>(p, cum, k);
