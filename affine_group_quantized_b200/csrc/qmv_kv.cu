@@ -5,10 +5,12 @@
 // are in qmv_kv_attn.cuh).  Contracts are in include/qmv.h.
 //
 // Append and read are streaming and element-wise: bf16 rows on one side, code
-// rows, scales and biases on the other.  A warp takes 32 chunks of 8 elements
-// of one token's heads (keys first, then values), so the token's sequence,
-// slot and page are looked up once for the warp; a group of 32, 64 or 128
-// elements is 4, 8 or 16 neighbouring lanes.
+// rows, scales and biases on the other, in chunks of 8 elements (16 bytes of
+// bf16).  A block takes a contiguous range of tokens, looks up where all of
+// them lie first (a thread each), and then goes through them with every thread
+// at a chunk of its own: its head and place in the head stay the same, so a
+// token costs it one row number.  A group of 32, 64 or 128 elements is 4, 8 or
+// 16 neighbouring lanes.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -29,6 +31,9 @@ namespace qmvc {
 namespace cg = cooperative_groups;
 
 constexpr int kRowThreads = 256;
+constexpr int kRowBatch = 256;    // tokens looked up at once
+constexpr int kRowAhead = 4;      // chunks of a thread in flight
+constexpr int kStartsMax = 1024;  // token_starts kept in shared memory up to here
 
 struct RowParams {
   CacheView c;
@@ -39,64 +44,54 @@ struct RowParams {
   int *positions;
   float *weights;
   int batch, tokens, state_width;
+  int block_tokens;           // tokens of a block
 };
 
-// Where token t goes: its sequence, slot, page and place in the page.  False
-// where it has none (padding, an unused row of the batch, or a bad index).
-struct Place {
-  int seq, slot, nth, page, at;
-};
+constexpr uint32_t kNowhere = 0xffffffffu;
 
-__device__ __forceinline__ bool place_of(const RowParams &p, int t, Place &o) {
-  int first = t;
-  o.seq = t;
+// The row of token t's slot for head 0, or kNowhere where it has none (padding,
+// an unused row of the batch, or a bad index).  `starts` may lie in shared
+// memory.  Writes the slot's state where there is one.
+__device__ __forceinline__ uint32_t place_of(const RowParams &p, const int *starts, int t) {
+  int seq = t, first = t;
   if (p.starts) {
     // the last sequence that starts at or before t
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(p.starts + mid) <= t) lo = mid;
+      if (starts[mid] <= t) lo = mid;
       else hi = mid;
     }
-    first = __ldg(p.starts + lo);
-    if (t < first || t >= __ldg(p.starts + lo + 1)) return false;
-    o.seq = lo;
-  } else {
-    first = t;
+    first = starts[lo];
+    if (t < first || t >= starts[lo + 1]) return kNowhere;
+    seq = lo;
   }
-  const int len = __ldg(p.lens + o.seq);
-  if (len < 0) return false;
-  o.nth = t - first;
-  const long long slot = static_cast<long long>(len) + o.nth;
-  if (slot >= static_cast<long long>(p.c.width) * p.c.S) {
+  const int len = __ldg(p.lens + seq);
+  if (len < 0) return kNowhere;
+  const int nth = t - first;
+  const long long at = static_cast<long long>(len) + nth;
+  if (at >= static_cast<long long>(p.c.width) * p.c.S) {
     if (p.c.status) atomicOr(p.c.status, 1);
-    return false;
+    return kNowhere;
   }
-  o.slot = static_cast<int>(slot);
-  const int at_page = o.slot / p.c.S;
-  o.at = o.slot - at_page * p.c.S;
-  o.page = checked_page(p.c, __ldg(p.c.table + static_cast<long long>(o.seq) * p.c.width + at_page));
-  return o.page >= 0;
+  const int slot = static_cast<int>(at), of = slot / p.c.S;
+  const int page = checked_page(p.c, __ldg(p.c.table + static_cast<long long>(seq) * p.c.width + of));
+  if (page < 0) return kNowhere;
+  if (p.positions) {
+    const int pos = __ldg(p.seen + seq) + nth;
+    for (int h = 0; h < p.c.H; ++h) {
+      const long long j = (static_cast<long long>(seq) * p.c.H + h) * p.state_width + slot;
+      p.positions[j] = pos;
+      p.weights[j] = 0.0f;
+    }
+  }
+  return cache_row(p.c, page, 0, slot - of * p.c.S);
 }
 
 // ---------------------------------------------------------------------------
 // The quantizer's binary32 steps, those of affine_quantize (qmv_quant.cu); the
 // rows of the two are tested to be the same bits
 // ---------------------------------------------------------------------------
-
-// min(round(d / scale), n_bins), halves away from zero: the product with the
-// rounded reciprocal is within 3 * 2^-24 of the quotient, so it decides the
-// code except near a half-integer, where the IEEE division does.
-__device__ __forceinline__ uint32_t code_of(float v, float bias, float scale, float rcp,
-                                            float n_bins) {
-  const float d = __fsub_rn(v, bias);
-  const float t = __fmul_rn(d, rcp);
-  const float r = rintf(t);
-  float code = r;
-  if (fabsf(__fsub_rn(t, r)) > 0.5f - fmaxf(fabsf(t), 1.0f) * 0x1p-20f)
-    code = roundf(__fdiv_rn(d, scale));
-  return static_cast<uint32_t>(fminf(code, n_bins));
-}
 
 // Scale and bias of a group with range [lo, hi], hi >= 0.
 __device__ __forceinline__ float2 scale_bias(float lo, float hi, float n_bins) {
@@ -107,100 +102,80 @@ __device__ __forceinline__ float2 scale_bias(float lo, float hi, float n_bins) {
   return q0 == 0.0f ? make_float2(step, 0.0f) : make_float2(__fdiv_rn(edge, q0), edge);
 }
 
-// ---------------------------------------------------------------------------
-// Append
-// ---------------------------------------------------------------------------
+// The codes of 8 elements, min(round((v - bias) / scale), n_bins) with halves
+// away from zero, as whole numbers.  The product with the rounded reciprocal is
+// within 3 * 2^-24 of the quotient, relative to it, so its nearest integer is
+// the code unless it lies within that of a half; elements within 2^-20 *
+// (n_bins + 1) of one take the IEEE division.  Adding and subtracting 1.5 * 2^23
+// rounds to the nearest integer (|t| < 2^22).
+template <int BITS>
+__device__ __forceinline__ void codes_of(float (&v)[8], float bias, float scale) {
+  constexpr float n_bins = static_cast<float>((1 << BITS) - 1);
+  constexpr float kSure = 0.5f - (n_bins + 1.0f) * 0x1p-20f, kRound = 12582912.0f;
+  const float rcp = __frcp_rn(scale);
+  float r[8];
+  bool sure = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = __fmul_rn(__fsub_rn(v[i], bias), rcp);
+    r[i] = __fsub_rn(__fadd_rn(t, kRound), kRound);
+    sure &= fabsf(__fsub_rn(t, r[i])) <= kSure;
+  }
+  if (!sure) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = __fsub_rn(v[i], bias);
+      const float t = __fmul_rn(d, rcp);
+      if (!(fabsf(__fsub_rn(t, r[i])) <= kSure)) r[i] = roundf(__fdiv_rn(d, scale));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fminf(r[i], n_bins);
+}
 
-// 8 bf16 elements in, 8 codes out (BITS bytes); the group's first lane stores
-// its scale and bias.  All lanes of the warp take part.
+// 8 bf16 elements in, 8 codes out (BITS bytes); s and b are the group's scale
+// and bias.  All lanes of the warp take part.
 template <int BITS, int GS>
-__device__ __forceinline__ uint2 quantize_chunk(const uint4 raw, int lane, uint16_t &s,
-                                                uint16_t &b) {
+__device__ __forceinline__ uint2 quantize_chunk(const uint4 raw, uint16_t &s, uint16_t &b) {
   constexpr float n_bins = static_cast<float>((1 << BITS) - 1);
   const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
+  // the range, in pairs (comparisons of bf16 are exact)
+  auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
+  __nv_bfloat162 lo2 = __hmin2(__hmin2(pair(pr[0]), pair(pr[1])), __hmin2(pair(pr[2]), pair(pr[3])));
+  __nv_bfloat162 hi2 = __hmax2(__hmax2(pair(pr[0]), pair(pr[1])), __hmax2(pair(pr[2]), pair(pr[3])));
+#pragma unroll
+  for (int o = 1; o < GS / 8; o <<= 1) {
+    lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+    hi2 = __hmax2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+  }
+  const float lo = fminf(__low2float(lo2), __high2float(lo2));
+  const float hi = fmaxf(fmaxf(__low2float(hi2), __high2float(hi2)), 0.0f);
+  const float2 sb = scale_bias(lo, hi, n_bins);
+  s = __bfloat16_as_ushort(__float2bfloat16_rn(sb.x));
+  b = __bfloat16_as_ushort(__float2bfloat16_rn(sb.y));
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(pr[i] << 16);
     v[2 * i + 1] = __uint_as_float(pr[i] & 0xffff0000u);
   }
-  float lo = __uint_as_float(0x7f7f0000u), hi = 0.0f;  // the largest finite bf16
+  codes_of<BITS>(v, sb.y, sb.x);
+  // 16 bits of codes are an exact binary32 number: packed by multiply-adds,
+  // taken out of the fraction under the exponent of 2^23
+  uint32_t half[BITS / 2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, v[i]);
-    hi = fmaxf(hi, v[i]);
+  for (int i = 0; i < BITS / 2; ++i) {
+    float x;
+    if constexpr (BITS == 4)
+      x = fmaf(v[4 * i + 3], 4096.0f, fmaf(v[4 * i + 2], 256.0f, fmaf(v[4 * i + 1], 16.0f, v[4 * i])));
+    else
+      x = fmaf(v[2 * i + 1], 256.0f, v[2 * i]);
+    half[i] = __float_as_uint(__fadd_rn(x, 8388608.0f));
   }
-#pragma unroll
-  for (int o = 1; o < GS / 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const float2 sb = scale_bias(lo, hi, n_bins);
-  s = __bfloat16_as_ushort(__float2bfloat16_rn(sb.x));
-  b = __bfloat16_as_ushort(__float2bfloat16_rn(sb.y));
-  const float rcp = __frcp_rn(sb.x);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i * BITS / 32] |= code_of(v[i], sb.y, sb.x, rcp, n_bins) << (i * BITS % 32);
-  return make_uint2(w[0], w[1]);
+  uint2 w = make_uint2(__byte_perm(half[0], half[1], 0x5410), 0u);
+  if constexpr (BITS == 8) w.y = __byte_perm(half[2], half[3], 0x5410);
+  return w;
 }
-
-template <int BITS, int GS, int D>
-__global__ void __launch_bounds__(kRowThreads) kv_append_kernel(const RowParams p) {
-  constexpr int kChunks = D / 8;  // chunks of a row
-  const int lane = threadIdx.x & 31;
-  const int side = p.c.H * kChunks;  // chunks of a token's keys
-  const int per_token = (2 * side + 31) / 32;
-  const long long items = static_cast<long long>(p.tokens) * per_token;
-  const long long warps = static_cast<long long>(gridDim.x) * (kRowThreads / 32);
-  wait_for_previous_grid();
-  for (long long it = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + threadIdx.x / 32;
-       it < items; it += warps) {
-    const int t = static_cast<int>(it / per_token), part = static_cast<int>(it - static_cast<long long>(t) * per_token);
-    Place o;
-    if (!place_of(p, t, o)) continue;
-    const int cc = part * 32 + lane;
-    const bool live = cc < 2 * side, value = cc >= side;
-    const int rest = value ? cc - side : cc;
-    const int h = rest / kChunks, i = rest - h * kChunks;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (live) {
-      const uint16_t *src = value ? p.v + t * p.v_stride : p.k + t * p.k_stride;
-      raw = __ldg(reinterpret_cast<const uint4 *>(src) + rest);
-    }
-    const long long row = cache_row(p.c, o.page, live ? h : 0, o.at);
-    uint8_t *dst = (value ? p.c.v : p.c.k) + row * (D * BITS / 8) + i * BITS;
-    if constexpr (BITS == 16) {
-      if (live) *reinterpret_cast<uint4 *>(dst) = raw;
-    } else {
-      uint16_t s, b;
-      const uint2 w = quantize_chunk<BITS, GS>(raw, lane, s, b);
-      if (live) {
-        if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(dst) = w.x;
-        else *reinterpret_cast<uint2 *>(dst) = w;
-        if (lane % (GS / 8) == 0) {
-          const long long g = row * (D / GS) + i / (GS / 8);
-          (value ? p.c.v_scales : p.c.k_scales)[g] = s;
-          (value ? p.c.v_biases : p.c.k_biases)[g] = b;
-        }
-      }
-    }
-    if (part == 0 && p.positions) {
-      const int pos = __ldg(p.seen + o.seq) + o.nth;
-      for (int hh = lane; hh < p.c.H; hh += 32) {
-        const long long j = (static_cast<long long>(o.seq) * p.c.H + hh) * p.state_width + o.slot;
-        p.positions[j] = pos;
-        p.weights[j] = 0.0f;
-      }
-    }
-  }
-  let_next_grid_start();
-}
-
-// ---------------------------------------------------------------------------
-// Read
-// ---------------------------------------------------------------------------
 
 // bf16(s * q + b) of 8 codes: the bf16 multiply-add rounds the exact value
 // once; codes enter as exact bf16 numbers (those of 8 bits through binary32).
@@ -208,20 +183,21 @@ template <int BITS>
 __device__ __forceinline__ uint4 dequantize_chunk(const uint2 w, uint16_t s, uint16_t b) {
   const __nv_bfloat16 sb = __ushort_as_bfloat16(s), bb = __ushort_as_bfloat16(b);
   const __nv_bfloat162 s2 = __halves2bfloat162(sb, sb), b2 = __halves2bfloat162(bb, bb);
+  auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
   uint32_t out[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     __nv_bfloat162 q;
     if constexpr (BITS == 4) {
-      const uint32_t m = ((w.x >> (8 * j)) & 0xfu) | (((w.x >> (8 * j + 4)) & 0xfu) << 16) | 0x43004300u;
-      const uint32_t one28 = 0x43004300u;
-      q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
-                  *reinterpret_cast<const __nv_bfloat162 *>(&one28));
+      // nibbles 2 j and 2 j + 1 under the exponent of 128: 128 + q
+      const uint32_t hi = j == 0 ? w.x << 12 : j == 1 ? w.x << 4 : j == 2 ? w.x >> 4 : w.x >> 12;
+      q = __hsub2(pair(((w.x >> (8 * j)) & 0xfu) | (hi & 0xf0000u) | 0x43004300u), pair(0x43004300u));
     } else {
       const uint32_t x = j < 2 ? w.x : w.y;
-      const uint32_t c0 = (x >> (16 * (j & 1))) & 0xffu, c1 = (x >> (16 * (j & 1) + 8)) & 0xffu;
-      q = __floats2bfloat162_rn(__fsub_rn(__uint_as_float(0x4b000000u | c0), 8388608.0f),
-                                __fsub_rn(__uint_as_float(0x4b000000u | c1), 8388608.0f));
+      const uint32_t c0 = __byte_perm(x, 0x4b000000u, j & 1 ? 0x7652 : 0x7650);
+      const uint32_t c1 = __byte_perm(x, 0x4b000000u, j & 1 ? 0x7653 : 0x7651);
+      q = __floats2bfloat162_rn(__fsub_rn(__uint_as_float(c0), 8388608.0f),
+                                __fsub_rn(__uint_as_float(c1), 8388608.0f));
     }
     const __nv_bfloat162 r = __hfma2(q, s2, b2);
     out[j] = *reinterpret_cast<const uint32_t *>(&r);
@@ -229,43 +205,107 @@ __device__ __forceinline__ uint4 dequantize_chunk(const uint2 w, uint16_t s, uin
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <int BITS, int D>
-__global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowParams p) {
-  constexpr int kChunks = D / 8;
-  const int lane = threadIdx.x & 31;
-  const int side = p.c.H * kChunks;
-  const int per_token = (2 * side + 31) / 32;
-  const long long items = static_cast<long long>(p.tokens) * per_token;
-  const long long warps = static_cast<long long>(gridDim.x) * (kRowThreads / 32);
-  const int group_chunks = BITS == 16 ? 1 : kChunks / p.c.G;
+// ---------------------------------------------------------------------------
+// Append and read
+// ---------------------------------------------------------------------------
+
+template <bool APPEND, int BITS, int GS, int D>
+__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowParams p) {
+  constexpr int kChunks = D / 8, kRow = D * BITS / 8;  // chunks and bytes of a row
+  constexpr int kGroups = D / GS, kLanes = GS / 8;     // groups of a row, lanes of a group
+  __shared__ uint32_t rows[kRowBatch];
+  __shared__ int starts[kStartsMax + 1];
+  const int tid = threadIdx.x;
+  const int side = p.c.H * kChunks, per_token = 2 * side;  // chunks of a token
+  // several tokens at once where a token has fewer chunks than the block threads
+  const int at_once = per_token < kRowThreads ? kRowThreads / per_token : 1;
+  const int sub = per_token < kRowThreads ? tid / per_token : 0;
+  const int mine = tid - sub * per_token;              // this thread's first chunk
+  const int t0 = blockIdx.x * p.block_tokens;
+  const int t1 = t0 + p.block_tokens < p.tokens ? t0 + p.block_tokens : p.tokens;
   wait_for_previous_grid();
-  for (long long it = static_cast<long long>(blockIdx.x) * (kRowThreads / 32) + threadIdx.x / 32;
-       it < items; it += warps) {
-    const int t = static_cast<int>(it / per_token), part = static_cast<int>(it - static_cast<long long>(t) * per_token);
-    Place o;
-    if (!place_of(p, t, o)) continue;
-    const int cc = part * 32 + lane;
-    if (cc >= 2 * side) continue;
-    const bool value = cc >= side;
-    const int rest = value ? cc - side : cc;
-    const int h = rest / kChunks, i = rest - h * kChunks;
-    const long long row = cache_row(p.c, o.page, h, o.at);
-    const uint8_t *src = (value ? p.c.v : p.c.k) + row * (D * BITS / 8) + i * BITS;
-    uint4 r;
-    if constexpr (BITS == 16) {
-      r = *reinterpret_cast<const uint4 *>(src);
-    } else {
-      uint2 w = make_uint2(0u, 0u);
-      if constexpr (BITS == 4) w.x = *reinterpret_cast<const uint32_t *>(src);
-      else w = *reinterpret_cast<const uint2 *>(src);
-      const long long g = row * p.c.G + i / group_chunks;
-      r = dequantize_chunk<BITS>(w, (value ? p.c.v_scales : p.c.k_scales)[g],
-                                 (value ? p.c.v_biases : p.c.k_biases)[g]);
-    }
-    uint16_t *dst = value ? p.v + t * p.v_stride : p.k + t * p.k_stride;
-    reinterpret_cast<uint4 *>(dst)[rest] = r;
+  const int *from = p.starts;
+  if (p.starts && p.batch <= kStartsMax) {
+    for (int i = tid; i <= p.batch; i += kRowThreads) starts[i] = __ldg(p.starts + i);
+    from = starts;
+    __syncthreads();
   }
-  let_next_grid_start();
+  for (int base = t0; base < t1; base += kRowBatch) {
+    const int count = t1 - base < kRowBatch ? t1 - base : kRowBatch;
+    if (tid < count) rows[tid] = place_of(p, from, base + tid);
+    __syncthreads();
+    // the warp's lanes stay together (groups are reduced across lanes)
+    for (int cc0 = 0; cc0 < per_token; cc0 += kRowThreads) {
+      const int cc = cc0 + mine;
+      const bool have = sub < at_once && cc < per_token;
+      const bool value = cc >= side;
+      const int rest = value ? cc - side : cc;
+      const int h = rest / kChunks, i = rest - h * kChunks;
+      uint8_t *codes = value ? p.c.v : p.c.k;
+      uint16_t *scales = value ? p.c.v_scales : p.c.k_scales;
+      uint16_t *biases = value ? p.c.v_biases : p.c.k_biases;
+      const uint32_t head_row = static_cast<uint32_t>(h) * p.c.S;
+      const long long stride = value ? p.v_stride : p.k_stride;
+      uint16_t *dense = (value ? p.v : p.k) + static_cast<long long>(base) * stride + rest * 8;
+      for (int n0 = 0; n0 < count; n0 += at_once * kRowAhead) {
+        uint32_t row[kRowAhead];
+        uint4 x[kRowAhead];
+        uint16_t s[kRowAhead], b[kRowAhead];
+#pragma unroll
+        for (int a = 0; a < kRowAhead; ++a) {
+          const int n = n0 + a * at_once + sub;
+          row[a] = have && n < count ? rows[n] : kNowhere;
+          x[a] = make_uint4(0u, 0u, 0u, 0u);
+          if (row[a] == kNowhere) continue;
+          row[a] += head_row;
+          if constexpr (APPEND) {
+            x[a] = __ldg(reinterpret_cast<const uint4 *>(dense + n * stride));
+          } else {
+            const uint8_t *src = codes + static_cast<unsigned long long>(row[a]) * kRow + i * BITS;
+            if constexpr (BITS == 16) {
+              x[a] = *reinterpret_cast<const uint4 *>(src);
+            } else {
+              if constexpr (BITS == 4) {
+                x[a].x = *reinterpret_cast<const uint32_t *>(src);
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                x[a].x = w.x;
+                x[a].y = w.y;
+              }
+              const unsigned long long g = static_cast<unsigned long long>(row[a]) * kGroups + i / kLanes;
+              s[a] = scales[g];
+              b[a] = biases[g];
+            }
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < kRowAhead; ++a) {
+          const int n = n0 + a * at_once + sub;
+          if constexpr (APPEND) {
+            uint8_t *dst = codes + static_cast<unsigned long long>(row[a]) * kRow + i * BITS;
+            if constexpr (BITS == 16) {
+              if (row[a] != kNowhere) *reinterpret_cast<uint4 *>(dst) = x[a];
+            } else {
+              const uint2 w = quantize_chunk<BITS, GS>(x[a], s[a], b[a]);
+              if (row[a] == kNowhere) continue;
+              if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(dst) = w.x;
+              else *reinterpret_cast<uint2 *>(dst) = w;
+              if (tid % kLanes == 0) {
+                const unsigned long long g = static_cast<unsigned long long>(row[a]) * kGroups + i / kLanes;
+                scales[g] = s[a];
+                biases[g] = b[a];
+              }
+            }
+          } else if (row[a] != kNowhere) {
+            uint4 *dst = reinterpret_cast<uint4 *>(dense + n * stride);
+            if constexpr (BITS == 16) *dst = x[a];
+            else *dst = dequantize_chunk<BITS>(make_uint2(x[a].x, x[a].y), s[a], b[a]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -673,42 +713,47 @@ int check_rows(const char *f, qmvc::RowParams &p, const void *k, const void *v, 
   return QMV_OK;
 }
 
-// One wave of 8 blocks per SM, or fewer blocks when there is less work.
-int row_grid(const qmvc::RowParams &p, int sms) {
-  const long long per_token = (2LL * p.c.H * (p.c.D / 8) + 31) / 32;
-  const long long need = (p.tokens * per_token + qmvc::kRowThreads / 32 - 1) / (qmvc::kRowThreads / 32);
-  return static_cast<int>(need < 8LL * sms ? need : 8LL * sms);
+// Blocks of the row kernels: about eight to an SM, each with a whole number of
+// passes over as many tokens as its threads hold at once.
+int row_grid(qmvc::RowParams &p, int sms) {
+  const int per_token = 2 * p.c.H * (p.c.D / 8);
+  const int at_once = per_token < qmvc::kRowThreads ? qmvc::kRowThreads / per_token : 1;
+  const long long blocks = 8LL * sms;
+  long long each = (p.tokens + blocks - 1) / blocks;
+  each = (each + at_once - 1) / at_once * at_once;
+  p.block_tokens = static_cast<int>(each);
+  return static_cast<int>((p.tokens + each - 1) / each);
 }
 
-template <int BITS, int GS, int D>
-cudaError_t append_t(const qmvc::RowParams &p, int grid, cudaStream_t st) {
-  if constexpr (BITS != 16 && D % GS != 0) return cudaErrorInvalidValue;  // refused before
+template <bool APPEND, int BITS, int GS, int D>
+cudaError_t rows_t(qmvc::RowParams &p, int sms, cudaStream_t st) {
+  if constexpr (D % GS != 0) return cudaErrorInvalidValue;  // refused before
   else
-    return qmvc::launch_overlapped(qmvc::kv_append_kernel<BITS, GS, D>, dim3(grid), qmvc::kRowThreads,
-                                   0, 1, st, p);
+    return qmvc::launch_overlapped(qmvc::kv_rows_kernel<APPEND, BITS, GS, D>, dim3(row_grid(p, sms)),
+                                   qmvc::kRowThreads, 0, 1, st, p);
 }
-template <int BITS, int GS>
-cudaError_t append_g(const qmvc::RowParams &p, int grid, cudaStream_t st) {
+template <bool APPEND, int BITS, int GS>
+cudaError_t rows_g(qmvc::RowParams &p, int sms, cudaStream_t st) {
   switch (p.c.D) {
-    case 64: return append_t<BITS, GS, 64>(p, grid, st);
-    case 96: return append_t<BITS, GS, 96>(p, grid, st);
-    case 128: return append_t<BITS, GS, 128>(p, grid, st);
-    default: return append_t<BITS, GS, 256>(p, grid, st);
+    case 64: return rows_t<APPEND, BITS, GS, 64>(p, sms, st);
+    case 96: return rows_t<APPEND, BITS, GS, 96>(p, sms, st);
+    case 128: return rows_t<APPEND, BITS, GS, 128>(p, sms, st);
+    default: return rows_t<APPEND, BITS, GS, 256>(p, sms, st);
   }
 }
-template <int BITS>
-cudaError_t append_b(const qmvc::RowParams &p, int grid, cudaStream_t st) {
-  const int gs = p.c.D / p.c.G;
-  return gs == 32 ? append_g<BITS, 32>(p, grid, st) : gs == 64 ? append_g<BITS, 64>(p, grid, st)
-                                                              : append_g<BITS, 128>(p, grid, st);
+template <bool APPEND, int BITS>
+cudaError_t rows_b(qmvc::RowParams &p, int sms, cudaStream_t st) {
+  switch (p.c.D / p.c.G) {
+    case 32: return rows_g<APPEND, BITS, 32>(p, sms, st);
+    case 64: return rows_g<APPEND, BITS, 64>(p, sms, st);
+    default: return rows_g<APPEND, BITS, 128>(p, sms, st);
+  }
 }
-template <int BITS>
-cudaError_t read_b(const qmvc::RowParams &p, int grid, cudaStream_t st) {
-  auto kern = p.c.D == 64    ? qmvc::kv_read_kernel<BITS, 64>
-              : p.c.D == 96  ? qmvc::kv_read_kernel<BITS, 96>
-              : p.c.D == 128 ? qmvc::kv_read_kernel<BITS, 128>
-                             : qmvc::kv_read_kernel<BITS, 256>;
-  return qmvc::launch_overlapped(kern, dim3(grid), qmvc::kRowThreads, 0, 1, st, p);
+template <bool APPEND>
+cudaError_t rows_launch(qmvc::RowParams &p, int sms, cudaStream_t st) {
+  return p.c.bits == 4   ? rows_b<APPEND, 4>(p, sms, st)
+         : p.c.bits == 8 ? rows_b<APPEND, 8>(p, sms, st)
+                         : rows_g<APPEND, 16, 32>(p, sms, st);  // bf16 rows have no groups
 }
 
 int check_state_width(const char *f, const qmvc::CacheView &c, int state_width) {
@@ -746,11 +791,7 @@ int kv_append(const qmv_kv_cache *cache, const void *k, const void *v, long long
   if (batch == 0 || num_tokens == 0) return kok();
   Device dev;
   if ((rc = current_device(f, &dev))) return rc;
-  const int grid = row_grid(p, dev.sms);
-  auto st = static_cast<cudaStream_t>(stream);
-  return launched(f, p.c.bits == 4    ? append_b<4>(p, grid, st)
-                     : p.c.bits == 8  ? append_b<8>(p, grid, st)
-                                      : append_g<16, 32>(p, grid, st));
+  return launched(f, rows_launch<true>(p, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, long long v_stride,
@@ -764,11 +805,7 @@ int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, lon
   if (batch == 0 || num_tokens == 0) return kok();
   Device dev;
   if ((rc = current_device(f, &dev))) return rc;
-  const int grid = row_grid(p, dev.sms);
-  auto st = static_cast<cudaStream_t>(stream);
-  return launched(f, p.c.bits == 4   ? read_b<4>(p, grid, st)
-                     : p.c.bits == 8 ? read_b<8>(p, grid, st)
-                                     : read_b<16>(p, grid, st));
+  return launched(f, rows_launch<false>(p, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 // What kv_attention and its workspace query share.
@@ -913,6 +950,12 @@ int qmv_kv_words(int call, int count, const long long *a) {
   auto ints = [&](int i) { return reinterpret_cast<int *>(a[i]); };
   auto floats = [&](int i) { return reinterpret_cast<float *>(a[i]); };
   auto num = [&](int i) { return static_cast<int>(a[i]); };
+  static const char *const kInts[4] = {"\x08\x09\x0a\x0e", "\x08\x09\x0a", "\x06\x07\x08\x0b",
+                                       "\x09\x0a\x0b\x0c\x0d\x0e"};  // words that are ints
+  if (call >= 0 && call < 4)
+    for (const char *i = kInts[call]; *i && *i < count; ++i)
+      if (a[static_cast<int>(*i)] != num(*i))
+        return kfail(QMV_ERR_SHAPE, "qmv_kv_words: a size of %lld is no int", a[static_cast<int>(*i)]);
   if (call == 0 && count == 17)
     return kv_append(cache(), ptr(1), ptr(2), a[3], a[4], ints(5), ints(6), ints(7), num(8), num(9),
                      num(10), ints(11), ints(12), floats(13), num(14), ints(15), ptr(16));
