@@ -5,12 +5,12 @@
 // are in qmv_kv_attn.cuh).  Contracts are in include/qmv.h.
 //
 // Append and read are streaming and element-wise: bf16 rows on one side, code
-// rows, scales and biases on the other, in chunks of 8 elements (16 bytes of
+// rows, scales and biases on the other, in chunks of 16 elements (32 bytes of
 // bf16).  A block takes a contiguous range of tokens, looks up where all of
 // them lie first (a thread each), and then goes through them with every thread
 // at a chunk of its own: its head and place in the head stay the same, so a
-// token costs it one row number.  A group of 32, 64 or 128 elements is 4, 8 or
-// 16 neighbouring lanes.
+// token costs it one row number.  A group of 32, 64 or 128 elements is 2, 4 or
+// 8 neighbouring lanes.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,7 +32,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kRowThreads = 256;
 constexpr int kRowBatch = 256;    // tokens looked up at once
-constexpr int kRowAhead = 4;      // chunks of a thread in flight
+constexpr int kRowAhead = 2;      // chunks of a thread in flight
 constexpr int kStartsMax = 1024;  // token_starts kept in shared memory up to here
 
 struct RowParams {
@@ -45,6 +45,7 @@ struct RowParams {
   float *weights;
   int batch, tokens, state_width;
   int block_tokens;           // tokens of a block
+  bool wide;                  // dense and bf16 rows lie at multiples of 32 bytes
 };
 
 constexpr uint32_t kNowhere = 0xffffffffu;
@@ -102,117 +103,157 @@ __device__ __forceinline__ float2 scale_bias(float lo, float hi, float n_bins) {
   return q0 == 0.0f ? make_float2(step, 0.0f) : make_float2(__fdiv_rn(edge, q0), edge);
 }
 
+// A chunk: 16 bf16 elements, or the words of 16 codes.
+struct Chunk {
+  uint32_t w[8];
+};
+
+// 32 bytes at once where they are aligned.  (Cache rows may be written in the
+// same kernel by no one else, but other kernels do: no read-only path.)
+__device__ __forceinline__ void load32(Chunk &x, const void *from, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]),
+                   "=r"(x.w[6]), "=r"(x.w[7])
+                 : "l"(from));
+  } else {
+    const uint4 a = static_cast<const uint4 *>(from)[0], b = static_cast<const uint4 *>(from)[1];
+    x.w[0] = a.x; x.w[1] = a.y; x.w[2] = a.z; x.w[3] = a.w;
+    x.w[4] = b.x; x.w[5] = b.y; x.w[6] = b.z; x.w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void *to, const Chunk &x, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to), "r"(x.w[0]),
+                 "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]), "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]), "r"(x.w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4 *>(to)[0] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    static_cast<uint4 *>(to)[1] = make_uint4(x.w[4], x.w[5], x.w[6], x.w[7]);
+  }
+}
+
 // The codes of 8 elements, min(round((v - bias) / scale), n_bins) with halves
 // away from zero, as whole numbers.  The product with the rounded reciprocal is
 // within 3 * 2^-24 of the quotient, relative to it, so its nearest integer is
-// the code unless it lies within that of a half; elements within 2^-20 *
+// the code unless it lies within that of a half; elements within 2^-22 *
 // (n_bins + 1) of one take the IEEE division.  Adding and subtracting 1.5 * 2^23
 // rounds to the nearest integer (|t| < 2^22).
 template <int BITS>
-__device__ __forceinline__ void codes_of(float (&v)[8], float bias, float scale) {
+__device__ __forceinline__ void codes_of(float (&v)[8], float bias, float scale, float rcp) {
   constexpr float n_bins = static_cast<float>((1 << BITS) - 1);
-  constexpr float kSure = 0.5f - (n_bins + 1.0f) * 0x1p-20f, kRound = 12582912.0f;
-  const float rcp = __frcp_rn(scale);
+  constexpr float kSure = 0.5f - (n_bins + 1.0f) * 0x1p-22f, kRound = 12582912.0f;
   float r[8];
-  bool sure = true;
+  float most = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = __fmul_rn(__fsub_rn(v[i], bias), rcp);
     r[i] = __fsub_rn(__fadd_rn(t, kRound), kRound);
-    sure &= fabsf(__fsub_rn(t, r[i])) <= kSure;
+    most = fmaxf(most, fabsf(__fsub_rn(t, r[i])));
   }
-  if (!sure) {
+  if (most > kSure) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = __fsub_rn(v[i], bias);
       const float t = __fmul_rn(d, rcp);
-      if (!(fabsf(__fsub_rn(t, r[i])) <= kSure)) r[i] = roundf(__fdiv_rn(d, scale));
+      if (fabsf(__fsub_rn(t, r[i])) > kSure) r[i] = roundf(__fdiv_rn(d, scale));
     }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = fminf(r[i], n_bins);
 }
 
-// 8 bf16 elements in, 8 codes out (BITS bytes); s and b are the group's scale
-// and bias.  All lanes of the warp take part.
-template <int BITS, int GS>
-__device__ __forceinline__ uint2 quantize_chunk(const uint4 raw, uint16_t &s, uint16_t &b) {
-  constexpr float n_bins = static_cast<float>((1 << BITS) - 1);
-  const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
-  // the range, in pairs (comparisons of bf16 are exact)
-  auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
-  __nv_bfloat162 lo2 = __hmin2(__hmin2(pair(pr[0]), pair(pr[1])), __hmin2(pair(pr[2]), pair(pr[3])));
-  __nv_bfloat162 hi2 = __hmax2(__hmax2(pair(pr[0]), pair(pr[1])), __hmax2(pair(pr[2]), pair(pr[3])));
+// The range of a group, its chunks in GS / 16 neighbouring lanes: (largest, and
+// at least 0; smallest).  In pairs of bf16, whose comparisons are exact.
+template <int GS>
+__device__ __forceinline__ float2 group_range(const Chunk &x) {
+  auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+  __nv_bfloat162 lo = pair(x.w[0]), hi = lo;
 #pragma unroll
-  for (int o = 1; o < GS / 8; o <<= 1) {
-    lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-    hi2 = __hmax2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+  for (int i = 1; i < 8; ++i) {
+    lo = __hmin2(lo, pair(x.w[i]));
+    hi = __hmax2(hi, pair(x.w[i]));
   }
-  const float lo = fminf(__low2float(lo2), __high2float(lo2));
-  const float hi = fmaxf(fmaxf(__low2float(hi2), __high2float(hi2)), 0.0f);
-  const float2 sb = scale_bias(lo, hi, n_bins);
-  s = __bfloat16_as_ushort(__float2bfloat16_rn(sb.x));
-  b = __bfloat16_as_ushort(__float2bfloat16_rn(sb.y));
-  float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(pr[i] << 16);
-    v[2 * i + 1] = __uint_as_float(pr[i] & 0xffff0000u);
+  for (int o = 1; o < GS / 16; o <<= 1) {
+    lo = __hmin2(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = __hmax2(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  codes_of<BITS>(v, sb.y, sb.x);
-  // 16 bits of codes are an exact binary32 number: packed by multiply-adds,
-  // taken out of the fraction under the exponent of 2^23
-  uint32_t half[BITS / 2];
-#pragma unroll
-  for (int i = 0; i < BITS / 2; ++i) {
-    float x;
-    if constexpr (BITS == 4)
-      x = fmaf(v[4 * i + 3], 4096.0f, fmaf(v[4 * i + 2], 256.0f, fmaf(v[4 * i + 1], 16.0f, v[4 * i])));
-    else
-      x = fmaf(v[2 * i + 1], 256.0f, v[2 * i]);
-    half[i] = __float_as_uint(__fadd_rn(x, 8388608.0f));
-  }
-  uint2 w = make_uint2(__byte_perm(half[0], half[1], 0x5410), 0u);
-  if constexpr (BITS == 8) w.y = __byte_perm(half[2], half[3], 0x5410);
-  return w;
+  return make_float2(fmaxf(fmaxf(__low2float(hi), __high2float(hi)), 0.0f),
+                     fminf(__low2float(lo), __high2float(lo)));
 }
 
-// bf16(s * q + b) of 8 codes: the bf16 multiply-add rounds the exact value
+// 16 bf16 elements to 16 codes (2 * BITS bytes), with the group's scale and bias.
+template <int BITS>
+__device__ __forceinline__ void quantize_chunk(Chunk &x, float scale, float bias, float rcp) {
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(x.w[4 * part + i] << 16);
+      v[2 * i + 1] = __uint_as_float(x.w[4 * part + i] & 0xffff0000u);
+    }
+    codes_of<BITS>(v, bias, scale, rcp);
+    // 16 bits of codes are an exact binary32 number: packed by multiply-adds,
+    // taken out of the fraction under the exponent of 2^23
+    uint32_t half[BITS / 2];
+#pragma unroll
+    for (int i = 0; i < BITS / 2; ++i) {
+      float y;
+      if constexpr (BITS == 4)
+        y = fmaf(v[4 * i + 3], 4096.0f, fmaf(v[4 * i + 2], 256.0f, fmaf(v[4 * i + 1], 16.0f, v[4 * i])));
+      else
+        y = fmaf(v[2 * i + 1], 256.0f, v[2 * i]);
+      half[i] = __float_as_uint(__fadd_rn(y, 8388608.0f));
+    }
+#pragma unroll
+    for (int i = 0; i < BITS / 4; ++i)
+      x.w[BITS / 4 * part + i] = __byte_perm(half[2 * i], half[2 * i + 1], 0x5410);
+  }
+}
+
+// bf16(s * q + b) of 16 codes: the bf16 multiply-add rounds the exact value
 // once; codes enter as exact bf16 numbers (those of 8 bits through binary32).
 template <int BITS>
-__device__ __forceinline__ uint4 dequantize_chunk(const uint2 w, uint16_t s, uint16_t b) {
+__device__ __forceinline__ void dequantize_chunk(Chunk &x, uint16_t s, uint16_t b) {
   const __nv_bfloat16 sb = __ushort_as_bfloat16(s), bb = __ushort_as_bfloat16(b);
   const __nv_bfloat162 s2 = __halves2bfloat162(sb, sb), b2 = __halves2bfloat162(bb, bb);
-  auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
-  uint32_t out[4];
+  auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+  uint32_t in[BITS / 2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int i = 0; i < BITS / 2; ++i) in[i] = x.w[i];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
     __nv_bfloat162 q;
     if constexpr (BITS == 4) {
-      // nibbles 2 j and 2 j + 1 under the exponent of 128: 128 + q
-      const uint32_t hi = j == 0 ? w.x << 12 : j == 1 ? w.x << 4 : j == 2 ? w.x >> 4 : w.x >> 12;
-      q = __hsub2(pair(((w.x >> (8 * j)) & 0xfu) | (hi & 0xf0000u) | 0x43004300u), pair(0x43004300u));
+      // both nibbles of a byte under the exponent of 128: 128 + q
+      const uint32_t w = in[j / 4], m = __byte_perm(w, w >> 4, j % 4 * 0x0101 + 0x0400);
+      q = __hsub2(pair((m & 0x000f000fu) | 0x43004300u), pair(0x43004300u));
     } else {
-      const uint32_t x = j < 2 ? w.x : w.y;
-      const uint32_t c0 = __byte_perm(x, 0x4b000000u, j & 1 ? 0x7652 : 0x7650);
-      const uint32_t c1 = __byte_perm(x, 0x4b000000u, j & 1 ? 0x7653 : 0x7651);
+      const uint32_t c0 = __byte_perm(in[j / 2], 0x4b000000u, j & 1 ? 0x7652 : 0x7650);
+      const uint32_t c1 = __byte_perm(in[j / 2], 0x4b000000u, j & 1 ? 0x7653 : 0x7651);
       q = __floats2bfloat162_rn(__fsub_rn(__uint_as_float(c0), 8388608.0f),
                                 __fsub_rn(__uint_as_float(c1), 8388608.0f));
     }
     const __nv_bfloat162 r = __hfma2(q, s2, b2);
-    out[j] = *reinterpret_cast<const uint32_t *>(&r);
+    x.w[j] = *reinterpret_cast<const uint32_t *>(&r);
   }
-  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // ---------------------------------------------------------------------------
 // Append and read
 // ---------------------------------------------------------------------------
 
+// Blocks of an SM: as many as leave the registers that the two directions need
+// (one fewer or more took 5 to 20 % longer).
+template <bool APPEND>
+constexpr int row_blocks() { return APPEND ? 4 : 5; }
+
 template <bool APPEND, int BITS, int GS, int D>
-__global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowParams p) {
-  constexpr int kChunks = D / 8, kRow = D * BITS / 8;  // chunks and bytes of a row
-  constexpr int kGroups = D / GS, kLanes = GS / 8;     // groups of a row, lanes of a group
+__global__ void __launch_bounds__(kRowThreads, row_blocks<APPEND>()) kv_rows_kernel(const RowParams p) {
+  constexpr int kChunks = D / 16, kRow = D * BITS / 8;  // chunks and bytes of a row
+  constexpr int kGroups = D / GS, kLanes = GS / 16;     // groups of a row, lanes of a group
   __shared__ uint32_t rows[kRowBatch];
   __shared__ int starts[kStartsMax + 1];
   const int tid = threadIdx.x;
@@ -246,31 +287,31 @@ __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowParams p)
       uint16_t *biases = value ? p.c.v_biases : p.c.k_biases;
       const uint32_t head_row = static_cast<uint32_t>(h) * p.c.S;
       const long long stride = value ? p.v_stride : p.k_stride;
-      uint16_t *dense = (value ? p.v : p.k) + static_cast<long long>(base) * stride + rest * 8;
+      uint16_t *dense = (value ? p.v : p.k) + static_cast<long long>(base) * stride + rest * 16;
       for (int n0 = 0; n0 < count; n0 += at_once * kRowAhead) {
         uint32_t row[kRowAhead];
-        uint4 x[kRowAhead];
+        Chunk x[kRowAhead];
         uint16_t s[kRowAhead], b[kRowAhead];
 #pragma unroll
         for (int a = 0; a < kRowAhead; ++a) {
           const int n = n0 + a * at_once + sub;
           row[a] = have && n < count ? rows[n] : kNowhere;
-          x[a] = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (APPEND) x[a] = Chunk{};
           if (row[a] == kNowhere) continue;
           row[a] += head_row;
           if constexpr (APPEND) {
-            x[a] = __ldg(reinterpret_cast<const uint4 *>(dense + n * stride));
+            load32(x[a], dense + n * stride, p.wide);
           } else {
-            const uint8_t *src = codes + static_cast<unsigned long long>(row[a]) * kRow + i * BITS;
+            const uint8_t *src = codes + static_cast<unsigned long long>(row[a]) * kRow + i * 2 * BITS;
             if constexpr (BITS == 16) {
-              x[a] = *reinterpret_cast<const uint4 *>(src);
+              load32(x[a], src, p.wide);
             } else {
               if constexpr (BITS == 4) {
-                x[a].x = *reinterpret_cast<const uint32_t *>(src);
-              } else {
                 const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                x[a].x = w.x;
-                x[a].y = w.y;
+                x[a].w[0] = w.x; x[a].w[1] = w.y;
+              } else {
+                const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                x[a].w[0] = w.x; x[a].w[1] = w.y; x[a].w[2] = w.z; x[a].w[3] = w.w;
               }
               const unsigned long long g = static_cast<unsigned long long>(row[a]) * kGroups + i / kLanes;
               s[a] = scales[g];
@@ -278,28 +319,45 @@ __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowParams p)
             }
           }
         }
+        // The groups' scales take three divisions and a reciprocal each: of the
+        // chunks in flight, lane a (mod 2) works out chunk a's, for all.
+        float scale = 0.0f, bias = 0.0f, rcp = 0.0f;
+        if constexpr (APPEND && BITS != 16) {
+          static_assert(kRowAhead == 2, "a lane for each chunk of a group's lanes");
+          const float2 r0 = group_range<GS>(x[0]), r1 = group_range<GS>(x[1]);
+          const float2 sb = scale_bias(tid & 1 ? r1.y : r0.y, tid & 1 ? r1.x : r0.x,
+                                       static_cast<float>((1 << BITS) - 1));
+          scale = sb.x;
+          bias = sb.y;
+          rcp = __frcp_rn(sb.x);
+        }
 #pragma unroll
         for (int a = 0; a < kRowAhead; ++a) {
           const int n = n0 + a * at_once + sub;
           if constexpr (APPEND) {
-            uint8_t *dst = codes + static_cast<unsigned long long>(row[a]) * kRow + i * BITS;
+            uint8_t *dst = codes + static_cast<unsigned long long>(row[a]) * kRow + i * 2 * BITS;
             if constexpr (BITS == 16) {
-              if (row[a] != kNowhere) *reinterpret_cast<uint4 *>(dst) = x[a];
+              if (row[a] != kNowhere) store32(dst, x[a], p.wide);
             } else {
-              const uint2 w = quantize_chunk<BITS, GS>(x[a], s[a], b[a]);
+              const int from = (tid & 30) | a;
+              const float sa = __shfl_sync(0xffffffffu, scale, from);
+              const float ba = __shfl_sync(0xffffffffu, bias, from);
+              const float ra = __shfl_sync(0xffffffffu, rcp, from);
               if (row[a] == kNowhere) continue;
-              if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(dst) = w.x;
-              else *reinterpret_cast<uint2 *>(dst) = w;
+              quantize_chunk<BITS>(x[a], sa, ba, ra);
+              if constexpr (BITS == 4)
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(x[a].w[0], x[a].w[1]);
+              else
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(x[a].w[0], x[a].w[1], x[a].w[2], x[a].w[3]);
               if (tid % kLanes == 0) {
                 const unsigned long long g = static_cast<unsigned long long>(row[a]) * kGroups + i / kLanes;
-                scales[g] = s[a];
-                biases[g] = b[a];
+                scales[g] = __bfloat16_as_ushort(__float2bfloat16_rn(sa));
+                biases[g] = __bfloat16_as_ushort(__float2bfloat16_rn(ba));
               }
             }
           } else if (row[a] != kNowhere) {
-            uint4 *dst = reinterpret_cast<uint4 *>(dense + n * stride);
-            if constexpr (BITS == 16) *dst = x[a];
-            else *dst = dequantize_chunk<BITS>(make_uint2(x[a].x, x[a].y), s[a], b[a]);
+            if constexpr (BITS != 16) dequantize_chunk<BITS>(x[a], s[a], b[a]);
+            store32(dense + n * stride, x[a], p.wide);
           }
         }
       }
@@ -322,6 +380,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_rows_kernel(const RowParams p)
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxCluster = 8;
+constexpr int kEvictCopies = 8;  // of a histogram: weights share few leading bytes
 constexpr int kEvictMaxSlots = 196608;
 
 struct EvictParams {
@@ -344,9 +403,54 @@ __device__ __forceinline__ uint32_t evict_key(float w, int pos, int sinks, int f
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictParams p) {
+// How a warp's lanes share out moves of `units` units each: `per` moves at once,
+// this lane at unit `at` of move `sub` of them (idle where sub == per).
+struct RowLanes {
+  int per, sub, at;
+  bool more;  // a move has 64 units: twice the lanes
+  __device__ __forceinline__ RowLanes(int units, int lane) {
+    more = units > 32;
+    const int u = more ? 32 : units > 0 ? units : 1;
+    per = 32 / u;
+    sub = lane / u;
+    at = lane - sub * u;
+    if (sub > per) sub = per;
+  }
+};
+
+// Units of type T of up to 4 * per moves, on their way from row rs to row rd of
+// lane m for move m; `base` is the lane's place in row 0.
+template <typename T>
+struct RowCopy {
+  T v[4];
+  uint32_t to[4];
+  __device__ __forceinline__ void load(const RowLanes &l, int m0, int count, uint32_t rs, uint32_t rd,
+                                       const T *base, int row_bytes) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int m = m0 + a * l.per + l.sub;
+      const uint32_t from = __shfl_sync(0xffffffffu, rs, m & 31);
+      to[a] = __shfl_sync(0xffffffffu, rd, m & 31);
+      if (m >= count || l.sub >= l.per) to[a] = kNowhere;
+      if (to[a] != kNowhere)
+        v[a] = *reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(base) +
+                                            static_cast<unsigned long long>(from) * row_bytes);
+    }
+  }
+  __device__ __forceinline__ void store(T *base, int row_bytes) const {
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (to[a] != kNowhere)
+        *reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(base) +
+                               static_cast<unsigned long long>(to[a]) * row_bytes) = v[a];
+  }
+};
+
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t smem[];
-  __shared__ uint32_t hist[2][256];
+  __shared__ uint32_t hist[2][256];                  // added up over the copies
+  __shared__ uint32_t copies[kEvictCopies][256];
+  __shared__ __align__(16) uint32_t total[256];      // over the cluster
   __shared__ uint32_t found[2];                      // digit, slots wanted within it
   __shared__ int warp_count[2][kEvictWarps];
   __shared__ int cta_count[3];                       // ties, holes, movers
@@ -390,30 +494,50 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
   const int from = p.seen[b] - p.recent;
   for (int i = tid; i < cnt; i += kEvictThreads)
     keys[i] = evict_key(w[lo + i], pos[lo + i], p.sinks, from);
-  for (int i = tid; i < 512; i += kEvictThreads) hist[i / 256][i % 256] = 0u;
+  for (int i = tid; i < kEvictCopies * 256; i += kEvictThreads) copies[i / 256][i % 256] = 0u;
   __syncthreads();
 
   // the key of the last kept slot, most significant byte first
   uint32_t prefix = 0u, want = static_cast<uint32_t>(left);
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    uint32_t *hg = hist[pass & 1];
     for (int i = tid; i < cnt; i += kEvictThreads) {
       const uint32_t k = keys[i];
       if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hg[(k >> shift) & 255u], 1u);
+        atomicAdd(&copies[tid % kEvictCopies][(k >> shift) & 255u], 1u);
     }
-    cluster.sync();
-    if (warp == 0) {
-      // lane l adds up bins 255 - 8 l downwards over the cluster
-      uint32_t bin[8], sum = 0u;
+    __syncthreads();
+    if (tid < 256) {
+      uint32_t sum = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        bin[i] = 0u;
-        for (int r = 0; r < C; ++r)
-          bin[i] += *cluster.map_shared_rank(&hg[255 - 8 * lane - i], r);
-        sum += bin[i];
+      for (int i = 0; i < kEvictCopies; ++i) {
+        sum += copies[i][tid];
+        copies[i][tid] = 0u;
       }
+      if (C == 1) total[tid] = sum;
+      else hist[pass & 1][tid] = sum;  // last read two passes ago
+    }
+    if (C > 1) {
+      cluster.sync();
+      if (tid < 256) {
+        uint32_t part[kEvictMaxCluster], sum = 0u;
+#pragma unroll
+        for (int r = 0; r < kEvictMaxCluster; ++r)
+          part[r] = r < C ? *cluster.map_shared_rank(&hist[pass & 1][tid], r) : 0u;
+#pragma unroll
+        for (int r = 0; r < kEvictMaxCluster; ++r) sum += part[r];
+        total[tid] = sum;
+      }
+    }
+    __syncthreads();
+    // lane l of the first warp goes through bins 255 - 8 l downwards
+    if (warp == 0) {
+      const uint4 hi = *reinterpret_cast<const uint4 *>(&total[252 - 8 * lane]);
+      const uint4 lo4 = *reinterpret_cast<const uint4 *>(&total[248 - 8 * lane]);
+      const uint32_t bin[8] = {hi.w, hi.z, hi.y, hi.x, lo4.w, lo4.z, lo4.y, lo4.x};
+      uint32_t sum = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += bin[i];
       uint32_t before = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -429,14 +553,10 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
         }
         before += bin[i];
       }
-    } else {
-      // the other buffer was last read before this pass's cluster.sync
-      for (int i = tid - 32; i < 256; i += kEvictThreads - 32) hist[(pass + 1) & 1][i] = 0u;
     }
     __syncthreads();
-    prefix |= found[0] << shift;
+    prefix |= found[0] << shift;  // (written again two barriers from here)
     want = found[1];
-    __syncthreads();
   }
 
   // slots with the last kept key: the first `want` of them stay
@@ -448,15 +568,15 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
   ties = __reduce_add_sync(0xffffffffu, ties);
   if (lane == 0) warp_count[0][warp] = ties;
   __syncthreads();
-  if (tid == 0) {
-    int sum = 0;
-    for (int i = 0; i < kEvictWarps; ++i) sum += warp_count[0][i];
-    cta_count[0] = sum;
+  if (warp == 0) {
+    const int sum = __reduce_add_sync(0xffffffffu, lane < kEvictWarps ? warp_count[0][lane] : 0);
+    if (lane == 0) cta_count[0] = sum;
   }
   cluster.sync();
-  int tie0 = 0;
-  for (int r = 0; r < rank; ++r) tie0 += *cluster.map_shared_rank(&cta_count[0], r);
-  for (int i = 0; i < warp; ++i) tie0 += warp_count[0][i];
+  // (lane r asks rank r, and lane i warp i)
+  int tie0 = lane < rank ? *cluster.map_shared_rank(&cta_count[0], lane) : 0;
+  tie0 += lane < warp ? warp_count[0][lane] : 0;
+  tie0 = __reduce_add_sync(0xffffffffu, tie0);
   __syncthreads();
 
   // holes and movers of this warp's slots, counted and then listed in order
@@ -478,15 +598,12 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
     warp_count[1][warp] = movers;
   }
   __syncthreads();
-  int hole0 = 0, mover0 = 0, all_holes = 0, all_movers = 0;
-  for (int i = 0; i < kEvictWarps; ++i) {
-    if (i == warp) {
-      hole0 = all_holes;
-      mover0 = all_movers;
-    }
-    all_holes += warp_count[0][i];
-    all_movers += warp_count[1][i];
-  }
+  const int lane_holes = lane < kEvictWarps ? warp_count[0][lane] : 0;
+  const int lane_movers = lane < kEvictWarps ? warp_count[1][lane] : 0;
+  int hole0 = __reduce_add_sync(0xffffffffu, lane < warp ? lane_holes : 0);
+  int mover0 = __reduce_add_sync(0xffffffffu, lane < warp ? lane_movers : 0);
+  const int all_holes = __reduce_add_sync(0xffffffffu, lane_holes);
+  const int all_movers = __reduce_add_sync(0xffffffffu, lane_movers);
   if (tid == 0) {
     cta_count[1] = all_holes;
     cta_count[2] = all_movers;
@@ -517,53 +634,85 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
   }
   cluster.sync();
 
-  // first hole and first mover of every CTA
-  int hole_at[kEvictMaxCluster + 1], mover_at[kEvictMaxCluster + 1];
-  hole_at[0] = mover_at[0] = 0;
+  // first hole and first mover of every CTA: lane r asks rank r
+  int holes_of = lane < C ? *cluster.map_shared_rank(&cta_count[1], lane) : 0;
+  int movers_of = lane < C ? *cluster.map_shared_rank(&cta_count[2], lane) : 0;
+  int hole_end = holes_of, mover_end = movers_of;
 #pragma unroll
-  for (int r = 0; r < kEvictMaxCluster; ++r) {
-    hole_at[r + 1] = hole_at[r] + (r < C ? *cluster.map_shared_rank(&cta_count[1], r) : 0);
-    mover_at[r + 1] = mover_at[r] + (r < C ? *cluster.map_shared_rank(&cta_count[2], r) : 0);
+  for (int o = 1; o < kEvictMaxCluster; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, hole_end, o), y = __shfl_up_sync(0xffffffffu, mover_end, o);
+    if (lane >= o) {
+      hole_end += x;
+      mover_end += y;
+    }
   }
-  const int moves = hole_at[kEvictMaxCluster];
+  const int moves = __shfl_sync(0xffffffffu, hole_end, C - 1);
   const int *table = p.c.table + static_cast<long long>(b) * p.c.width;
-  for (int m = rank * kEvictWarps + warp; m < moves; m += C * kEvictWarps) {
-    int rh = 0, rm = 0, h0 = 0, m0 = 0, nh = hole_at[1];
+  // The cluster's warps share the moves evenly; a warp looks up to 32 of them up
+  // at once, a lane each, and then copies their rows, 16 bytes a lane, four
+  // lines of them in flight.  A lane's place in a row (or rows) is always the
+  // same.
+  const RowLanes big(p.c.row_bytes / 8, lane), small(4 * p.c.G, lane);
+  uint8_t *side = big.at < p.c.row_bytes / 16 ? p.c.k + big.at * 16 : p.c.v + big.at * 16 - p.c.row_bytes;
+  const int kind = p.c.G ? small.at / p.c.G : 0;
+  uint16_t *scale = kind == 0   ? p.c.k_scales
+                    : kind == 1 ? p.c.k_biases
+                    : kind == 2 ? p.c.v_scales
+                                : p.c.v_biases;
+  scale += p.c.G ? small.at - kind * p.c.G : 0;
+  const int each = (moves + C * kEvictWarps - 1) / (C * kEvictWarps);
+  const int m_end = (rank * kEvictWarps + warp + 1) * each < moves ? (rank * kEvictWarps + warp + 1) * each : moves;
+  for (int m0 = (rank * kEvictWarps + warp) * each; m0 < m_end; m0 += 32) {
+    const int count = m_end - m0 < 32 ? m_end - m0 : 32;
+    uint32_t rs = kNowhere, rd = kNowhere;
+    // the ranks that list the move's hole and mover, and where their lists begin
+    const int m = m0 + lane;
+    int rh = 0, rm = 0, h0 = 0, l0 = -__shfl_sync(0xffffffffu, holes_of, 0);
 #pragma unroll
     for (int r = 1; r < kEvictMaxCluster; ++r) {
-      if (m >= hole_at[r] && r < C) {
+      const int he = __shfl_sync(0xffffffffu, hole_end, r - 1), me = __shfl_sync(0xffffffffu, mover_end, r - 1);
+      const int holes_r = __shfl_sync(0xffffffffu, holes_of, r);
+      if (r < C && m >= he) {
         rh = r;
-        h0 = hole_at[r];
+        h0 = he;
       }
-      if (m >= mover_at[r] && r < C) {
+      if (r < C && m >= me) {
         rm = r;
-        m0 = mover_at[r];
-        nh = hole_at[r + 1] - hole_at[r];
+        l0 = me - holes_r;  // movers come after the rank's holes
       }
     }
-    const int dst = static_cast<int>(cluster.map_shared_rank(list, rh)[m - h0]);
-    const int src = static_cast<int>(cluster.map_shared_rank(list, rm)[nh + m - m0]);
-    if (lane == 0) {
+    if (lane < count) {
+      const int dst = static_cast<int>(cluster.map_shared_rank(list, rh)[m - h0]);
+      const int src = static_cast<int>(cluster.map_shared_rank(list, rm)[m - l0]);
+      const int ps = src / p.c.S, pd = dst / p.c.S;
+      const int sp = checked_page(p.c, __ldg(table + ps)), dp = checked_page(p.c, __ldg(table + pd));
       const float x = w[src];
       const int y = pos[src];
       new_w[dst] = x;
       new_pos[dst] = y;
+      if (sp >= 0 && dp >= 0) {
+        rs = cache_row(p.c, sp, h, src - ps * p.c.S);
+        rd = cache_row(p.c, dp, h, dst - pd * p.c.S);
+      }
     }
-    const int sp = checked_page(p.c, __ldg(table + src / p.c.S));
-    const int dp = checked_page(p.c, __ldg(table + dst / p.c.S));
-    if (sp < 0 || dp < 0) continue;
-    const long long rs = cache_row(p.c, sp, h, src % p.c.S), rd = cache_row(p.c, dp, h, dst % p.c.S);
-    const int units = p.c.row_bytes / 16;
-    for (int i = lane; i < 2 * units; i += 32) {
-      uint8_t *side = i < units ? p.c.k : p.c.v;
-      const int at = i < units ? i : i - units;
-      reinterpret_cast<uint4 *>(side + rd * p.c.row_bytes)[at] =
-          reinterpret_cast<const uint4 *>(side + rs * p.c.row_bytes)[at];
-    }
-    for (int i = lane; i < 4 * p.c.G; i += 32) {
-      const int a = i / p.c.G, g = i - a * p.c.G;
-      uint16_t *s = a == 0 ? p.c.k_scales : a == 1 ? p.c.k_biases : a == 2 ? p.c.v_scales : p.c.v_biases;
-      s[rd * p.c.G + g] = s[rs * p.c.G + g];
+    for (int half = 0; half < (big.more ? 2 : 1); ++half) {
+      // (a row of more than 32 units, of bf16 heads of 256: keys, then values)
+      uint4 *rows = reinterpret_cast<uint4 *>(half ? p.c.v + big.at * 16 : side);
+      RowCopy<uint4> x;
+      RowCopy<uint16_t> y;
+      // the first lines of both kinds together, then what is left of each
+      x.load(big, 0, count, rs, rd, rows, p.c.row_bytes);
+      if (p.c.G) y.load(small, 0, count, rs, rd, scale, 2 * p.c.G);
+      x.store(rows, p.c.row_bytes);
+      if (p.c.G) y.store(scale, 2 * p.c.G);
+      for (int i = 4 * big.per; i < count; i += 4 * big.per) {
+        x.load(big, i, count, rs, rd, rows, p.c.row_bytes);
+        x.store(rows, p.c.row_bytes);
+      }
+      for (int i = 4 * small.per; p.c.G && i < count; i += 4 * small.per) {
+        y.load(small, i, count, rs, rd, scale, 2 * p.c.G);
+        y.store(scale, 2 * p.c.G);
+      }
     }
   }
   cluster.sync();  // every mover's state has been read, and every list
@@ -710,15 +859,19 @@ int check_rows(const char *f, qmvc::RowParams &p, const void *k, const void *v, 
   p.starts = starts;
   p.batch = batch;
   p.tokens = tokens;
+  p.wide = k_stride % 16 == 0 && v_stride % 16 == 0 && aligned(k, 32) && aligned(v, 32) &&
+           (p.c.bits != 16 || (aligned(p.c.k, 32) && aligned(p.c.v, 32)));
   return QMV_OK;
 }
 
-// Blocks of the row kernels: about eight to an SM, each with a whole number of
-// passes over as many tokens as its threads hold at once.
+// One wave of blocks, each with a whole number of passes over as many tokens as
+// its threads hold at once (a block begins with look-ups that depend on one
+// another: more and shorter blocks only repeat those).
+template <bool APPEND>
 int row_grid(qmvc::RowParams &p, int sms) {
-  const int per_token = 2 * p.c.H * (p.c.D / 8);
+  const int per_token = 2 * p.c.H * (p.c.D / 16);
   const int at_once = per_token < qmvc::kRowThreads ? qmvc::kRowThreads / per_token : 1;
-  const long long blocks = 8LL * sms;
+  const long long blocks = static_cast<long long>(qmvc::row_blocks<APPEND>()) * sms;
   long long each = (p.tokens + blocks - 1) / blocks;
   each = (each + at_once - 1) / at_once * at_once;
   p.block_tokens = static_cast<int>(each);
@@ -729,7 +882,7 @@ template <bool APPEND, int BITS, int GS, int D>
 cudaError_t rows_t(qmvc::RowParams &p, int sms, cudaStream_t st) {
   if constexpr (D % GS != 0) return cudaErrorInvalidValue;  // refused before
   else
-    return qmvc::launch_overlapped(qmvc::kv_rows_kernel<APPEND, BITS, GS, D>, dim3(row_grid(p, sms)),
+    return qmvc::launch_overlapped(qmvc::kv_rows_kernel<APPEND, BITS, GS, D>, dim3(row_grid<APPEND>(p, sms)),
                                    qmvc::kRowThreads, 0, 1, st, p);
 }
 template <bool APPEND, int BITS, int GS>
@@ -901,6 +1054,7 @@ int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens,
     return kfail(QMV_ERR_SHAPE, "%s: budget=%d recent=%d sinks=%d: need recent + sinks <= budget", f,
                  budget, recent, sinks);
   if ((rc = check_state_width(f, p.c, state_width))) return rc;
+  constexpr int kEvictSlots = 2048;
   const int room = table_width * p.c.S;
   if (room > qmvc::kEvictMaxSlots)
     return kfail(QMV_ERR_UNSUPPORTED, "%s: room of %d slots above %d", f, room, qmvc::kEvictMaxSlots);
@@ -922,14 +1076,22 @@ int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens,
   p.budget = budget;
   p.recent = recent;
   p.sinks = sinks;
-  // a CTA for every 2048 slots of room, up to the portable cluster size
+  // A CTA for every kEvictSlots slots of room, up to the portable cluster size,
+  // while all clusters fit the device at once (two CTAs to an SM, less what
+  // clusters of 8 leave unused: 32 rows of 16384 slots took 32 us in clusters of
+  // 8, which ran in two waves), and at least as many as hold the keys.
   int cluster = 1;
-  while (cluster < qmvc::kEvictMaxCluster && cluster * 2048 < room) cluster *= 2;
+  const long long rows = static_cast<long long>(batch) * p.c.H;
+  while (cluster < qmvc::kEvictMaxCluster && cluster * kEvictSlots < room &&
+         (2 * cluster * rows <= 2 * dev.sms || room > cluster * (qmvc::kEvictMaxSlots / qmvc::kEvictMaxCluster)))
+    cluster *= 2;
   p.seg_max = ((room + cluster - 1) / cluster + 31) & ~31;
   const size_t smem = 8u * static_cast<size_t>(p.seg_max);
-  const cudaError_t e = cudaFuncSetAttribute(qmvc::kv_evict_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(qmvc::kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e == cudaSuccess)  // two CTAs to an SM
+    e = cudaFuncSetAttribute(qmvc::kv_evict_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return kfail(QMV_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", f, cudaGetErrorString(e));
