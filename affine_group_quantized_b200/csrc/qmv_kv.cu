@@ -382,6 +382,7 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxCluster = 8;
 constexpr int kEvictCopies = 8;  // of a histogram: weights share few leading bytes
 constexpr int kEvictMaxSlots = 196608;
+constexpr int kEvictPool = 256;
 
 struct EvictParams {
   CacheView c;
@@ -451,7 +452,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
   __shared__ uint32_t hist[2][256];                  // added up over the copies
   __shared__ uint32_t copies[kEvictCopies][256];
   __shared__ __align__(16) uint32_t total[256];      // over the cluster
-  __shared__ uint32_t found[2];                      // digit, slots wanted within it
+  __shared__ uint32_t found[3];                      // digit, slots wanted within it, slots
+  __shared__ uint32_t near[kEvictPool], pool[kEvictPool];  // keys around the last kept one: here, of all
+  __shared__ int near_count;
   __shared__ int warp_count[2][kEvictWarps];
   __shared__ int cta_count[3];                       // ties, holes, movers
   uint32_t *keys = smem, *list = smem + p.seg_max;   // holes first, then movers
@@ -491,15 +494,31 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
     return;
   }
 
+  // The state of the slots below the new length is written now, as if all of
+  // them stayed (the moves overwrite the others'), and the rest is cleared: at
+  // once, or behind the moves where the buffers are the same.
   const int from = p.seen[b] - p.recent;
-  for (int i = tid; i < cnt; i += kEvictThreads)
-    keys[i] = evict_key(w[lo + i], pos[lo + i], p.sinks, from);
+  const bool in_place = new_w == w || new_pos == pos;
+#pragma unroll 2
+  for (int i = tid; i < cnt; i += kEvictThreads) {
+    const float x = w[lo + i];
+    const int y = pos[lo + i];
+    keys[i] = evict_key(x, y, p.sinks, from);
+    if (lo + i < left) {
+      new_w[lo + i] = x;
+      new_pos[lo + i] = y;
+    } else if (!in_place) {
+      new_w[lo + i] = 0.0f;
+      new_pos[lo + i] = -1;
+    }
+  }
   for (int i = tid; i < kEvictCopies * 256; i += kEvictThreads) copies[i / 256][i % 256] = 0u;
+  if (tid == 0) near_count = 0;
   __syncthreads();
 
   // the key of the last kept slot, most significant byte first
-  uint32_t prefix = 0u, want = static_cast<uint32_t>(left);
-  for (int pass = 0; pass < 4; ++pass) {
+  uint32_t prefix = 0u, want = static_cast<uint32_t>(left), count = 0u;
+  for (int pass = 0; pass < 4 && want != count; ++pass) {
     const int shift = 24 - 8 * pass;
     for (int i = tid; i < cnt; i += kEvictThreads) {
       const uint32_t k = keys[i];
@@ -550,6 +569,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
         if (before < want && want <= before + bin[i]) {
           found[0] = static_cast<uint32_t>(255 - 8 * lane - i);
           found[1] = want - before;
+          found[2] = bin[i];
         }
         before += bin[i];
       }
@@ -557,27 +577,74 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
     __syncthreads();
     prefix |= found[0] << shift;  // (written again two barriers from here)
     want = found[1];
+    count = found[2];  // keys that begin with the prefix: `want` of them stay
+    if (pass > 0 && pass < 3 && want != count && count <= kEvictPool) {
+      // few enough to be brought together and ranked: a thread counts how many
+      // are above its key
+      for (int i = tid; i < cnt; i += kEvictThreads)
+        if ((keys[i] >> shift) == (prefix >> shift)) near[atomicAdd(&near_count, 1)] = keys[i];
+      if (C > 1) cluster.sync();
+      else __syncthreads();
+      const int n_of = lane < C ? *cluster.map_shared_rank(&near_count, lane) : 0;
+      int end = n_of;
+#pragma unroll
+      for (int o = 1; o < kEvictMaxCluster; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += x;
+      }
+      if (warp < C) {  // warp r fetches rank r's
+        const int n_r = __shfl_sync(0xffffffffu, n_of, warp), at = __shfl_sync(0xffffffffu, end, warp) - n_r;
+        const uint32_t *from_r = cluster.map_shared_rank(near, warp);
+        for (int i = lane; i < n_r; i += 32) pool[at + i] = from_r[i];
+      }
+      __syncthreads();
+      if (tid < static_cast<int>(count)) {
+        const uint32_t k = pool[tid];
+        uint32_t above = 0u, alike = 0u;
+        for (uint32_t i = 0; i < count; ++i) {
+          above += pool[i] > k;
+          alike += pool[i] == k;
+        }
+        if (above < want && want <= above + alike) {  // the same for all alike
+          found[0] = k;
+          found[1] = want - above;
+          found[2] = alike;
+        }
+      }
+      __syncthreads();
+      prefix = found[0];
+      want = found[1];
+      count = found[2];
+      break;
+    }
   }
+  // every key that begins with the prefix stays: no tie to be broken
+  const bool all_stay = want == count;
 
   // slots with the last kept key: the first `want` of them stay
   const int span = ((cnt + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
   const int w0 = warp * span < cnt ? warp * span : cnt;
   const int w1 = w0 + span < cnt ? w0 + span : cnt;
-  int ties = 0;
-  for (int i = w0 + lane; i < w1; i += 32) ties += keys[i] == prefix;
-  ties = __reduce_add_sync(0xffffffffu, ties);
-  if (lane == 0) warp_count[0][warp] = ties;
-  __syncthreads();
-  if (warp == 0) {
-    const int sum = __reduce_add_sync(0xffffffffu, lane < kEvictWarps ? warp_count[0][lane] : 0);
-    if (lane == 0) cta_count[0] = sum;
+  int tie0 = 0;
+  if (!all_stay) {
+    int ties = 0;
+    for (int i = w0 + lane; i < w1; i += 32) ties += keys[i] == prefix;
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    if (lane == 0) warp_count[0][warp] = ties;
+    __syncthreads();
+    if (warp == 0) {
+      const int sum = __reduce_add_sync(0xffffffffu, lane < kEvictWarps ? warp_count[0][lane] : 0);
+      if (lane == 0) cta_count[0] = sum;
+    }
+    cluster.sync();
+    // (lane r asks rank r, and lane i warp i)
+    tie0 = lane < rank ? *cluster.map_shared_rank(&cta_count[0], lane) : 0;
+    tie0 += lane < warp ? warp_count[0][lane] : 0;
+    tie0 = __reduce_add_sync(0xffffffffu, tie0);
+    __syncthreads();
+  } else {
+    want = 0x7fffffffu;
   }
-  cluster.sync();
-  // (lane r asks rank r, and lane i warp i)
-  int tie0 = lane < rank ? *cluster.map_shared_rank(&cta_count[0], lane) : 0;
-  tie0 += lane < warp ? warp_count[0][lane] : 0;
-  tie0 = __reduce_add_sync(0xffffffffu, tie0);
-  __syncthreads();
 
   // holes and movers of this warp's slots, counted and then listed in order
   int holes = 0, movers = 0, tie = tie0;
@@ -625,12 +692,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
     if (mover) list[mover0 + __popc(mm & under)] = static_cast<uint32_t>(lo + i);
     hole0 += __popc(mh);
     mover0 += __popc(mm);
-    if (keep && below) {
-      const float x = w[lo + i];
-      const int y = pos[lo + i];
-      new_w[lo + i] = x;
-      new_pos[lo + i] = y;
-    }
   }
   cluster.sync();
 
@@ -685,14 +746,21 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
       const int dst = static_cast<int>(cluster.map_shared_rank(list, rh)[m - h0]);
       const int src = static_cast<int>(cluster.map_shared_rank(list, rm)[m - l0]);
       const int ps = src / p.c.S, pd = dst / p.c.S;
-      const int sp = checked_page(p.c, __ldg(table + ps)), dp = checked_page(p.c, __ldg(table + pd));
+      const int es = __ldg(table + ps), ed = __ldg(table + pd);
       const float x = w[src];
       const int y = pos[src];
+      const int sp = checked_page(p.c, es), dp = checked_page(p.c, ed);
       new_w[dst] = x;
       new_pos[dst] = y;
       if (sp >= 0 && dp >= 0) {
         rs = cache_row(p.c, sp, h, src - ps * p.c.S);
         rd = cache_row(p.c, dp, h, dst - pd * p.c.S);
+        // all of the rows on their way at once
+        for (int i = 0; count > 4 && i < p.c.row_bytes; i += 128) {
+          const unsigned long long at = static_cast<unsigned long long>(rs) * p.c.row_bytes + i;
+          asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.c.k + at));
+          asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.c.v + at));
+        }
       }
     }
     for (int half = 0; half < (big.more ? 2 : 1); ++half) {
@@ -716,7 +784,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
     }
   }
   cluster.sync();  // every mover's state has been read, and every list
-  for (int i = (lo > left ? lo : left) + tid; i < hi; i += kEvictThreads) {
+  for (int i = (lo > left ? lo : left) + tid; in_place && i < hi; i += kEvictThreads) {
     new_w[i] = 0.0f;
     new_pos[i] = -1;
   }
