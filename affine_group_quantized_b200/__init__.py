@@ -16,7 +16,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqmv.so")
@@ -92,9 +91,7 @@ def lib() -> ctypes.CDLL:
                                    ctypes.c_size_t, P, P]
         L.kv_attention_workspace.argtypes = [C, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
         L.kv_evict.argtypes = [C] + [P] * 8 + [I] * 6 + [P, P]
-        L.qmv_kv_words.argtypes = [I, I, ctypes.c_char_p]
-        for f in (L.kv_append, L.kv_read, L.kv_attention, L.kv_attention_workspace, L.kv_evict,
-                  L.qmv_kv_words):
+        for f in (L.kv_append, L.kv_read, L.kv_attention, L.kv_attention_workspace, L.kv_evict):
             f.restype = I
         L.qmv_kv_last_error.restype = ctypes.c_char_p
         L.qmv_kv_last_error.argtypes = []
@@ -306,76 +303,27 @@ def _device_of(t):
     return t.device.index
 
 
-def _on_device(cache):
-    """The current device must be the cache's: a launch goes to the current
-    device.  Returns the cache's device, or None for plain addresses."""
-    want = cache._device
-    if want is not None:
+_native = None
+
+
+def _kv():
+    """The module with the kv_* calls' argument checks (csrc/kv_native.c)."""
+    global _native
+    if _native is None:
+        lib()  # the library it calls
+        try:
+            from . import _kv_native
+        except ImportError as e:
+            raise RuntimeError(
+                f"the binding's _kv_native module is missing ({e}): build it with "
+                "`python -m affine_group_quantized_b200.build`") from e
         import torch
-        here = torch.cuda.current_device()
-        if here != want:
-            raise ValueError(f"the cache is on device {want}, the current device is {here}")
-    return want
-
-
-def _arg(name, t, nbytes, size, device):
-    """The address of an argument of at least nbytes, contiguous, of `size`-byte
-    elements (None: any), on the cache's device."""
-    if t is None:
-        return 0
-    if isinstance(t, int):
-        return t
-    if t.nbytes < nbytes:
-        raise ValueError(f"{name}: {t.nbytes} bytes, the call needs {nbytes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if size is not None and t.element_size() != size:
-        raise ValueError(f"{name}: must hold {size}-byte values")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name}: not on the cache's device {device}")
-    return t.data_ptr()
-
-
-def _arg_rows(name, t, stride, rows, heads, dim, device):
-    """Address and stride (elements) between the rows of a bf16 [rows, heads,
-    dim] argument whose heads lie behind one another: a tensor's own stride, or
-    the one given (heads * dim when none is)."""
-    packed = heads * dim
-    if t is None or isinstance(t, int):
-        return t or 0, packed if stride is None else stride
-    if stride is None and t.dim() == 3 and t.shape == (rows, heads, dim):
-        if t.element_size() != 2:
-            raise ValueError(f"{name}: must hold bf16 values")
-        s0, s1, s2 = t.stride()
-        if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
-            raise ValueError(f"{name}: a row's heads must be contiguous")
-        if device is not None and t.get_device() != device:
-            raise ValueError(f"{name}: not on the cache's device {device}")
-        return t.data_ptr(), s0 if rows > 1 else packed
-    stride = packed if stride is None else stride
-    need = 2 * ((rows - 1) * stride + packed) if rows > 0 else 0
-    return _arg(name, t, need, 2, device), stride
-
-
-def _kv_stream(stream, device):
-    """`stream`, or the current stream of the cache's device."""
-    if stream is None and device is not None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
-    return _stream(stream) or 0
-
-
-# the calls of qmv_kv_words by number, and how their arguments are laid out
-_APPEND, _READ, _ATTENTION, _EVICT = range(4)
-_WORDS = (struct.Struct("17q"), struct.Struct("13q"), struct.Struct("16q"), struct.Struct("17q"))
-_FLOAT, _FLOAT_BITS = struct.Struct("f"), struct.Struct("i")
-_KV_NAMES = ("kv_append", "kv_read", "kv_attention", "kv_evict")
-
-
-def _kv_call(call, *words):
-    rc = lib().qmv_kv_words(call, len(words), _WORDS[call].pack(*words))
-    if rc != QMV_OK:
-        _check_kv(_KV_NAMES[call], rc)
+        _kv_native.setup(
+            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+            getattr(torch._C, "_cuda_getCurrentRawStream",
+                    lambda d: torch.cuda.current_stream(d).cuda_stream))
+        _native = _kv_native
+    return _native
 
 
 def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
@@ -384,34 +332,22 @@ def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, t
     """Write num_tokens new tokens' keys and values into the cache: sequence b's
     tokens token_starts[b] .. token_starts[b+1]-1 (one token each without
     token_starts) fill its slots from lens[b] on (see include/qmv.h)."""
-    H, D = cache.num_kv_heads, cache.head_dim
-    dev = _on_device(cache)
-    kp, ks = _arg_rows("k", k, k_stride, num_tokens, H, D, dev)
-    vp, vs = _arg_rows("v", v, v_stride, num_tokens, H, D, dev)
-    state = 4 * batch * H * state_width
-    _kv_call(_APPEND, cache._address, kp, vp, ks, vs,
-             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
-             _arg("lens", lens, 4 * batch, 4, dev),
-             _arg("token_starts", token_starts, 4 * batch + 4, 4, dev),
-             batch, num_tokens, table_width, _arg("seen", seen, 4 * batch, 4, dev),
-             _arg("positions", positions, state, 4, dev), _arg("weights", weights, state, 4, dev),
-             state_width, _arg("d_status", d_status, 4, 4, dev), _kv_stream(stream, dev))
+    rc = (_native or _kv()).append(
+        cache._address, cache._device, k, v, block_table, lens, token_starts, batch, num_tokens,
+        table_width, seen, positions, weights, state_width, k_stride, v_stride, d_status, stream)
+    if rc:
+        _check_kv("kv_append", rc)
 
 
 def kv_read(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
             k_stride=None, v_stride=None, d_status=None, stream=None):
     """Slots lens[b] .. of sequence b as dense bf16 rows token_starts[b] ..
     token_starts[b+1]-1 of k and v: the reverse of kv_append."""
-    H, D = cache.num_kv_heads, cache.head_dim
-    dev = _on_device(cache)
-    kp, ks = _arg_rows("k", k, k_stride, num_tokens, H, D, dev)
-    vp, vs = _arg_rows("v", v, v_stride, num_tokens, H, D, dev)
-    _kv_call(_READ, cache._address, kp, vp, ks, vs,
-             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
-             _arg("lens", lens, 4 * batch, 4, dev),
-             _arg("token_starts", token_starts, 4 * batch + 4, 4, dev),
-             batch, num_tokens, table_width, _arg("d_status", d_status, 4, 4, dev),
-             _kv_stream(stream, dev))
+    rc = (_native or _kv()).read(
+        cache._address, cache._device, k, v, block_table, lens, token_starts, batch, num_tokens,
+        table_width, k_stride, v_stride, d_status, stream)
+    if rc:
+        _check_kv("kv_read", rc)
 
 
 def kv_attention_workspace(cache, batch, num_q_heads, table_width, with_weights=False) -> int:
@@ -429,19 +365,11 @@ def kv_attention(cache, q, block_table, lens, out, batch, num_q_heads, table_wid
     """Attention of one new token per sequence over its lens[b] slots; with
     weights, each slot's probabilities are added to them (see include/qmv.h).
     workspace: a tensor of kv_attention_workspace's bytes."""
-    H, D = cache.num_kv_heads, cache.head_dim
-    if workspace is None or isinstance(workspace, int):
-        raise ValueError("workspace: must be a tensor")
-    dev = _on_device(cache)
-    qp, qs = _arg_rows("q", q, q_stride, batch, num_q_heads, D, dev)
-    _kv_call(_ATTENTION, cache._address, qp, qs,
-             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
-             _arg("lens", lens, 4 * batch, 4, dev),
-             _arg("out", out, 2 * batch * num_q_heads * D, 2, dev),
-             batch, num_q_heads, table_width, _FLOAT_BITS.unpack(_FLOAT.pack(scale))[0],
-             _arg("weights", weights, 4 * batch * H * state_width, 4, dev), state_width,
-             _arg("workspace", workspace, 0, None, dev), workspace.nbytes,
-             _arg("d_status", d_status, 4, 4, dev), _kv_stream(stream, dev))
+    rc = (_native or _kv()).attention(
+        cache._address, cache._device, q, block_table, lens, out, batch, num_q_heads,
+        table_width, scale, workspace, weights, state_width, q_stride, d_status, stream)
+    if rc:
+        _check_kv("kv_attention", rc)
 
 
 def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_weights,
@@ -450,15 +378,9 @@ def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_w
     """Keep the `budget` slots of every (sequence, kv head) with the largest
     weights, the newest `recent` and first `sinks` positions before all
     others, and move them below budget (see include/qmv.h)."""
-    dev = _on_device(cache)
-    state = 4 * batch * cache.num_kv_heads * state_width
-    _kv_call(_EVICT, cache._address,
-             _arg("block_table", block_table, 4 * batch * table_width, 4, dev),
-             _arg("lens", lens, 4 * batch, 4, dev), _arg("seen", seen, 4 * batch, 4, dev),
-             _arg("weights", weights, state, 4, dev),
-             _arg("positions", positions, state, 4, dev),
-             _arg("new_lens", new_lens, 4 * batch, 4, dev),
-             _arg("new_weights", new_weights, state, 4, dev),
-             _arg("new_positions", new_positions, state, 4, dev),
-             batch, table_width, state_width, budget, recent, sinks,
-             _arg("d_status", d_status, 4, 4, dev), _kv_stream(stream, dev))
+    rc = (_native or _kv()).evict(
+        cache._address, cache._device, block_table, lens, seen, weights, positions, new_lens,
+        new_weights, new_positions, batch, table_width, state_width, budget, recent, sinks,
+        d_status, stream)
+    if rc:
+        _check_kv("kv_evict", rc)

@@ -1,4 +1,5 @@
-"""Build libqmv.so (the sm_100a kernels and the C ABI) in-tree with nvcc.
+"""Build libqmv.so (the sm_100a kernels and the C ABI) in-tree with nvcc, and
+the CPython module of the binding's kv_* calls with the host compiler.
 
 The library is compiled for sm_100a only.  It is placed next to this file so
 that it travels with the repository and is the one the Python binding loads.
@@ -8,15 +9,18 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqmv.so")
+NATIVE = os.path.join(HERE, "_kv_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["qmv_api.cu", "qmv_quant.cu", "qmv_qmm.cu", "qmv_kv.cu", "qmv_kv_attn4.cu",
            "qmv_kv_attn8.cu", "qmv_kv_attn16.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CC = os.environ.get("CC", "gcc")
 
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -34,9 +38,9 @@ def _inputs():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB):
+    if not force and os.path.exists(LIB) and os.path.exists(NATIVE):
         newest = max(os.path.getmtime(f) for f in _inputs())
-        if os.path.getmtime(LIB) >= newest:
+        if min(os.path.getmtime(LIB), os.path.getmtime(NATIVE)) >= newest:
             return LIB
     # one object per source, compiled side by side, then one link
     objdir = os.path.join(HERE, "_build")
@@ -57,6 +61,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             "-o", LIB + ".tmp", *objs]
     subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
+    # the module calls libqmv.so, found beside it
+    subprocess.run([CC, "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                    "-I", INCLUDE, "-o", NATIVE + ".tmp", os.path.join(CSRC, "kv_native.c"),
+                    "-L", HERE, "-l:libqmv.so", "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(NATIVE + ".tmp", NATIVE)
     return LIB
 
 

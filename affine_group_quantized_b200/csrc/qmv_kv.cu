@@ -19,7 +19,6 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
-#include <cstring>
 #include <mutex>
 #include <string>
 
@@ -1170,40 +1169,5 @@ int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens,
 }
 
 const char *qmv_kv_last_error(void) { return g_kv_error.c_str(); }
-
-// The calls above with their arguments as 64-bit words, in order (a float as
-// its bits): for the Python binding, which pays for every argument it passes.
-// The words' number is the binding's to get right; it is checked here.
-int qmv_kv_words(int call, int count, const long long *a) {
-  auto cache = [&] { return reinterpret_cast<const qmv_kv_cache *>(a[0]); };
-  auto ptr = [&](int i) { return reinterpret_cast<void *>(a[i]); };
-  auto ints = [&](int i) { return reinterpret_cast<int *>(a[i]); };
-  auto floats = [&](int i) { return reinterpret_cast<float *>(a[i]); };
-  auto num = [&](int i) { return static_cast<int>(a[i]); };
-  static const char *const kInts[4] = {"\x08\x09\x0a\x0e", "\x08\x09\x0a", "\x06\x07\x08\x0b",
-                                       "\x09\x0a\x0b\x0c\x0d\x0e"};  // words that are ints
-  if (call >= 0 && call < 4)
-    for (const char *i = kInts[call]; *i && *i < count; ++i)
-      if (a[static_cast<int>(*i)] != num(*i))
-        return kfail(QMV_ERR_SHAPE, "qmv_kv_words: a size of %lld is no int", a[static_cast<int>(*i)]);
-  if (call == 0 && count == 17)
-    return kv_append(cache(), ptr(1), ptr(2), a[3], a[4], ints(5), ints(6), ints(7), num(8), num(9),
-                     num(10), ints(11), ints(12), floats(13), num(14), ints(15), ptr(16));
-  if (call == 1 && count == 13)
-    return kv_read(cache(), ptr(1), ptr(2), a[3], a[4], ints(5), ints(6), ints(7), num(8), num(9),
-                   num(10), ints(11), ptr(12));
-  if (call == 2 && count == 16) {
-    float scale;
-    const int bits = num(9);
-    static_assert(sizeof scale == sizeof bits, "a float's bits");
-    std::memcpy(&scale, &bits, sizeof scale);
-    return kv_attention(cache(), ptr(1), a[2], ints(3), ints(4), ptr(5), num(6), num(7), num(8), scale,
-                        floats(10), num(11), ptr(12), static_cast<size_t>(a[13]), ints(14), ptr(15));
-  }
-  if (call == 3 && count == 17)
-    return kv_evict(cache(), ints(1), ints(2), ints(3), floats(4), ints(5), ints(6), floats(7), ints(8),
-                    num(9), num(10), num(11), num(12), num(13), num(14), ints(15), ptr(16));
-  return kfail(QMV_ERR_SHAPE, "qmv_kv_words: call %d with %d words", call, count);
-}
 
 }  // extern "C"
