@@ -1173,6 +1173,7 @@ attn_kernel(const AttnParams p) {
   Segment<C> sg;
   if (u0 < u1) {
     Cursor k = cursor_at<C>(p, cum, known, u0);
+    sg.load(p, k, lane);
     Fetcher<C> fetch;
     fetch.start(p, k, u1 - u0, lane);
     const uint32_t ring_end = ring + C::STAGES * C::STAGE;
@@ -1188,7 +1189,7 @@ attn_kernel(const AttnParams p) {
       ahead = ahead + C::STAGE == ring_end ? ring : ahead + C::STAGE;
       if (u < u0) continue;
       if (fresh) {
-        sg.load(p, k, lane);
+        if (u > u0) sg.load(p, k, lane);
         sg.begin(p, lane);
         fresh = false;
       }
@@ -1225,19 +1226,26 @@ attn_kernel(const AttnParams p) {
 
   // Join the pieces of a segment, in the order of its slots: piece 2 w (+ 1) is
   // warp w's first (last).  First each piece's factor for each head ...
+  // A segment's pieces are the last ones of neighbouring warps and then, where
+  // it ends, the first one of the next.
   const int mine = lane < 2 * C::WARPS ? piece_seg[lane & 1][lane >> 1] : -1;
   const unsigned all = __ballot_sync(0xffffffffu, mine >= 0);
+  const unsigned alike = __match_any_sync(0xffffffffu, mine);
+#pragma unroll 1
   for (int i = tid; i < 2 * C::WARPS * C::HEADS; i += C::WARPS * 32) {
-    const int j = i / C::HEADS, h = i % C::HEADS, seg = piece_seg[j & 1][j >> 1];
-    if (seg < 0) continue;
+    const int j = i / C::HEADS, h = i % C::HEADS;  // a whole warp takes this step or none
+    const unsigned run = __shfl_sync(0xffffffffu, alike, j);
+    if (!((all >> j) & 1u)) continue;
+    const int j0 = __ffs(run) - 1, j1 = 31 - __clz(run);
+    // (pieces between that are not there count nothing)
     float m = kNegInf, l = 0.0f;
 #pragma unroll 4
-    for (int r = 0; r < 2 * C::WARPS; ++r)
-      if (piece_seg[r & 1][r >> 1] == seg) m = fmaxf(m, piece_ml[r & 1][r >> 1][h].x);
+    for (int r = j0; r <= j1; ++r)
+      if ((run >> r) & 1u) m = fmaxf(m, piece_ml[r & 1][r >> 1][h].x);
     const float ms = m == kNegInf ? 0.0f : m;
 #pragma unroll 4
-    for (int r = 0; r < 2 * C::WARPS; ++r)
-      if (piece_seg[r & 1][r >> 1] == seg) {
+    for (int r = j0; r <= j1; ++r)
+      if ((run >> r) & 1u) {
         const float2 ml = piece_ml[r & 1][r >> 1][h];
         l += ex2(ml.x - ms) * ml.y;
       }
@@ -1247,12 +1255,14 @@ attn_kernel(const AttnParams p) {
   __syncthreads();
   // ... then four sums a thread.
   int cut0 = -1, cut1 = -1;
+#pragma unroll 1
   for (unsigned left = all; left;) {
     const int j0 = __ffs(left) - 1;
     const int seg = __shfl_sync(0xffffffffu, mine, j0);
-    const unsigned run = __ballot_sync(0xffffffffu, mine == seg);
+    const unsigned run = __shfl_sync(0xffffffffu, alike, j0);
     left &= ~run;
-    const int j1 = 31 - __clz(run);
+    const unsigned lasts = run & 0xaaaaaaaau, ends = run & 0x55555555u;
+    const int w0 = lasts ? (__ffs(lasts) - 1) >> 1 : 0, some = __popc(lasts);
     const int b = seg / unit, hc = seg - b * unit;
     const int tiles = (cum[b + 1] - cum[b]) / unit;
     const int first = cum[b] + hc * tiles;
@@ -1268,11 +1278,12 @@ attn_kernel(const AttnParams p) {
       const int h = quad_head<C>(q);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-      for (int j = j0; j <= j1; ++j) {
-        if (!((run >> j) & 1u)) continue;
-        const float4 *from = (j & 1) ? tails + (j >> 1) * C::QUADS
-                                     : p.warp_o + static_cast<long long>(cta_warp + (j >> 1)) * C::QUADS;
-        add_quad(o, *reinterpret_cast<const float2 *>(&factor[j][h]), from[q]);
+      for (int w = w0; w < w0 + some; ++w)
+        add_quad(o, *reinterpret_cast<const float2 *>(&factor[2 * w + 1][h]), tails[w * C::QUADS + q]);
+      if (ends) {
+        const int w = (__ffs(ends) - 1) >> 1;
+        add_quad(o, *reinterpret_cast<const float2 *>(&factor[2 * w][h]),
+                 p.warp_o[static_cast<long long>(cta_warp + w) * C::QUADS + q]);
       }
       if (whole)
         store_quad<C>(p.out + head * C::D, p.R - r0, q, o, joined[j0][h].y, joined[j0][h + 1].y);
