@@ -877,26 +877,22 @@ int check_cache(const char *f, const qmv_kv_cache *c, const int *table, int batc
   return QMV_OK;
 }
 
-// SM count and shared-memory limit of the current device, asked once per device.
-struct Device {
-  int sms = 0, smem_optin = 0;
-};
+using qmvc::Device;
+
+// The current device and its SM count, asked once per device.
 int current_device(const char *f, Device *out) {
-  constexpr int kMaxDevices = 64;
-  static Device devs[kMaxDevices];
-  static std::once_flag once[kMaxDevices];
+  static int sms[qmvc::kMaxDevices];
+  static std::once_flag once[qmvc::kMaxDevices];
   int d = 0;
   const cudaError_t e = cudaGetDevice(&d);
-  if (e != cudaSuccess || d < 0 || d >= kMaxDevices)
+  if (e != cudaSuccess || d < 0 || d >= qmvc::kMaxDevices)
     return kfail(QMV_ERR_CUDA, "%s: no usable CUDA device (%s)", f, cudaGetErrorString(e));
   std::call_once(once[d], [&] {
-    if (cudaDeviceGetAttribute(&devs[d].sms, cudaDevAttrMultiProcessorCount, d) != cudaSuccess ||
-        cudaDeviceGetAttribute(&devs[d].smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d) !=
-            cudaSuccess)
-      devs[d].sms = 0;
+    if (cudaDeviceGetAttribute(&sms[d], cudaDevAttrMultiProcessorCount, d) != cudaSuccess) sms[d] = 0;
   });
-  if (devs[d].sms <= 0) return kfail(QMV_ERR_CUDA, "%s: cannot query device %d", f, d);
-  *out = devs[d];
+  if (sms[d] <= 0) return kfail(QMV_ERR_CUDA, "%s: cannot query device %d", f, d);
+  out->id = d;
+  out->sms = sms[d];
   return QMV_OK;
 }
 
@@ -1102,9 +1098,9 @@ int kv_attention(const qmv_kv_cache *cache, const void *q, long long q_stride,
   a.state_width = state_width;
   a.workspace = workspace;
   a.stream = static_cast<cudaStream_t>(stream);
-  return launched(f, a.cache.bits == 4   ? qmvc::attn_launch_4(a, dev.sms)
-                     : a.cache.bits == 8 ? qmvc::attn_launch_8(a, dev.sms)
-                                         : qmvc::attn_launch_16(a, dev.sms));
+  return launched(f, a.cache.bits == 4   ? qmvc::attn_launch_4(a, dev)
+                     : a.cache.bits == 8 ? qmvc::attn_launch_8(a, dev)
+                                         : qmvc::attn_launch_16(a, dev));
 }
 
 int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens, const int *seen,
@@ -1154,15 +1150,9 @@ int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens,
     cluster *= 2;
   p.seg_max = ((room + cluster - 1) / cluster + 31) & ~31;
   const size_t smem = 8u * static_cast<size_t>(p.seg_max);
-  cudaError_t e = cudaFuncSetAttribute(qmvc::kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e == cudaSuccess)  // two CTAs to an SM
-    e = cudaFuncSetAttribute(qmvc::kv_evict_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return kfail(QMV_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", f, cudaGetErrorString(e));
-  }
+  static qmvc::Granted granted;
+  const cudaError_t e = allow_smem(qmvc::kv_evict_kernel, granted, dev, static_cast<int>(smem));
+  if (e != cudaSuccess) return kfail(QMV_ERR_CUDA, "%s: shared memory: %s", f, cudaGetErrorString(e));
   return launched(f, qmvc::launch_overlapped(qmvc::kv_evict_kernel, dim3(batch * p.c.H * cluster),
                                              qmvc::kEvictThreads, smem, cluster,
                                              static_cast<cudaStream_t>(stream), p));

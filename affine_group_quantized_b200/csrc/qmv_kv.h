@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -61,14 +62,37 @@ struct AttnArgs {
   cudaStream_t stream;
 };
 
+// What the launches ask of a device, once.
+constexpr int kMaxDevices = 64;
+struct Device {
+  int id = 0, sms = 0;
+};
+
+// Allows a kernel `bytes` of dynamic shared memory on a device, and once allowed
+// does not ask again (one `granted` per kernel; two threads may both ask).
+struct Granted {
+  std::atomic<int> bytes[kMaxDevices];
+};
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kern)(KArgs...), Granted &granted, const Device &dev, int bytes) {
+  if (bytes <= granted.bytes[dev.id].load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)  // as many blocks of an SM as the rest allows
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) granted.bytes[dev.id].store(bytes, std::memory_order_relaxed);
+  else cudaGetLastError();  // clear it
+  return e;
+}
+
 // Bytes of workspace a call needs, and the launches themselves, by width
 // (qmv_kv_attn4.cu, 8 and 16).
 size_t attn_workspace_4(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
 size_t attn_workspace_8(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
 size_t attn_workspace_16(const CacheView &c, int batch, int num_q_heads, bool weights, int sms);
-cudaError_t attn_launch_4(const AttnArgs &a, int sms);
-cudaError_t attn_launch_8(const AttnArgs &a, int sms);
-cudaError_t attn_launch_16(const AttnArgs &a, int sms);
+cudaError_t attn_launch_4(const AttnArgs &a, const Device &dev);
+cudaError_t attn_launch_8(const AttnArgs &a, const Device &dev);
+cudaError_t attn_launch_16(const AttnArgs &a, const Device &dev);
 
 // A launch that may be scheduled while the previous kernel of the stream
 // finishes: the kernels hold their first global access until then

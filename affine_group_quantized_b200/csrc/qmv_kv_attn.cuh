@@ -89,11 +89,16 @@ struct AttnCfg {
   static constexpr int G = BITS == 16 ? 0 : D / GS;    // groups of a row
   static constexpr int RB = D * BITS / 8;              // bytes of a row
   static constexpr int CH = RB / 16;                   // 16-byte chunks of a row
-  // accumulators of at most 32 registers leave room for 16 warps on an SM
-  static constexpr bool SMALL = D * NB <= 128 && BITS != 16;
-  static constexpr int WARPS = BITS == 16 && D == 256 ? 4 : 8;
-  static constexpr int CTAS_PER_SM = SMALL ? 2 : 1;
-  static constexpr int ROOM = (SMALL ? 110592 : 204800) / WARPS;  // bytes of a warp's ring
+  // Warps of an SM, by the registers of the accumulators: 16 in two CTAs where
+  // they are 16 (128 registers a thread: heads of 64 took 28.4 us for 52 MB, 29.1
+  // with 12 warps), 12 where they are up to 32 (168: heads of 128 took 126 us for
+  // 604 MB and 47.7 us for 168 MB in groups of 32, with 16 warps 132 and 56.9 us),
+  // else 8.  bf16 rows need few instructions and deep rings: 8, and 4 for heads
+  // of 256, whose tiles are 16 KB.
+  static constexpr bool LIGHT = BITS != 16 && D * NB <= 64, SMALL = BITS != 16 && D * NB <= 128;
+  static constexpr int WARPS = LIGHT ? 8 : SMALL ? 12 : BITS == 16 && D == 256 ? 4 : 8;
+  static constexpr int CTAS_PER_SM = LIGHT ? 2 : 1;
+  static constexpr int ROOM = (LIGHT ? 110592 : SMALL ? 196608 : 204800) / WARPS;  // bytes of a warp's ring
   // 4-bit tiles are 32 slots where three of them fit: half as many softmax
   // steps for the same bytes
   static constexpr int SLOT = 2 * RB + 8 * G;          // bytes of a slot
@@ -109,6 +114,7 @@ struct AttnCfg {
   static_assert(STAGES >= 2, "a tile is fetched while another is computed");
   static constexpr int TAIL = HEADS * D * 4;           // a warp's last piece
   static constexpr int SMEM = WARPS * (STAGES * STAGE > TAIL ? STAGES * STAGE : TAIL);
+  static_assert(SMEM + 4 * 4097 + 6144 <= 232448, "rings, the tiles' sums of 4096 sequences, and the rest");
   static constexpr int MT = D / 16;                    // 16-element accumulator tiles
   static constexpr int QUADS = HEADS * D / 4;          // float4 of a piece
   // elements that one set of value words covers
@@ -612,21 +618,21 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
     }
   }
   if (p.scores) {
-    const int hk = k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS;
+    const int hk = p.chunks == 1 ? k.hc : k.hc / p.chunks, r0 = (k.hc - hk * p.chunks) * C::HEADS + 2 * t;
+    float *to = p.scores + (static_cast<long long>(k.b) * p.Hq + hk * p.R + r0) * p.room + t0 + row;
+    const int have = k.n - t0 - row;  // slots behind this lane's first that count
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = r0 + nb * 8 + 2 * t + (j & 1);
-        if (r < p.R) {
-          float *to = p.scores + (static_cast<long long>(k.b) * p.Hq + hk * p.R + r) * p.room + t0;
+      for (int i = 0; i < 2; ++i)
+        if (r0 + nb * 8 + i < p.R) {
+          float *at = to + (nb * 8 + i) * p.room;
 #pragma unroll
-          for (int blk = 0; blk < C::TB; ++blk) {
-            const int at = 16 * blk + row + 8 * (j >> 1);
-            if (t0 + at < k.n) to[at] = s[blk][nb][j] * sg.f[nb][j & 1];
-          }
+          for (int blk = 0; blk < C::TB; ++blk)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              if (16 * blk + 8 * half < have) at[16 * blk + 8 * half] = s[blk][nb][i + 2 * half] * sg.f[nb][i];
         }
-      }
   }
 
   // The running maximum is looked at lane by lane: only when some lane's slots
@@ -1476,7 +1482,7 @@ size_t lay_out(AttnParams &p, const CacheView &c, int batch, int num_q_heads, bo
 }
 
 template <class C>
-cudaError_t attn_run(const AttnArgs &a, int sms) {
+cudaError_t attn_run(const AttnArgs &a, const Device &dev) {
   AttnParams p = {};
   p.c = a.cache;
   p.q = static_cast<const __nv_bfloat16 *>(a.q);
@@ -1494,16 +1500,13 @@ cudaError_t attn_run(const AttnArgs &a, int sms) {
   p.weights = a.weights;
   p.state_width = a.state_width;
   p.room = static_cast<long long>(a.cache.width) * a.cache.S;
-  p.ctas = attn_ctas<C>(sms);
-  lay_out<C>(p, a.cache, a.batch, a.num_q_heads, a.weights != nullptr, sms,
+  p.ctas = attn_ctas<C>(dev.sms);
+  lay_out<C>(p, a.cache, a.batch, a.num_q_heads, a.weights != nullptr, dev.sms,
              static_cast<uint8_t *>(a.workspace));
   const size_t smem = C::SMEM + 4 * (static_cast<size_t>(a.batch) + 1);
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return e;
-  }
+  static Granted granted;
+  cudaError_t e = allow_smem(attn_kernel<C>, granted, dev, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   e = launch_overlapped(attn_kernel<C>, dim3(p.ctas), C::WARPS * 32, smem, 1, a.stream, p);
   if (e != cudaSuccess) return e;
   const int weight_blocks =
@@ -1554,9 +1557,9 @@ size_t attn_workspace_bits(const CacheView &c, int batch, int num_q_heads, bool 
   });
 }
 template <int BITS>
-cudaError_t attn_launch_bits(const AttnArgs &a, int sms) {
+cudaError_t attn_launch_bits(const AttnArgs &a, const Device &dev) {
   return attn_select<BITS>(a.cache, a.num_q_heads / a.cache.H,
-                           [&](auto cfg) { return attn_run<decltype(cfg)>(a, sms); });
+                           [&](auto cfg) { return attn_run<decltype(cfg)>(a, dev); });
 }
 
 }  // namespace qmvc

@@ -6,6 +6,6 @@ namespace qmvc {
 size_t attn_workspace_16(const CacheView &c, int batch, int num_q_heads, bool weights, int sms) {
   return attn_workspace_bits<16>(c, batch, num_q_heads, weights, sms);
 }
-cudaError_t attn_launch_16(const AttnArgs &a, int sms) { return attn_launch_bits<16>(a, sms); }
+cudaError_t attn_launch_16(const AttnArgs &a, const Device &dev) { return attn_launch_bits<16>(a, dev); }
 
 }  // namespace qmvc

@@ -75,8 +75,8 @@ class HostCache:
         if self.bits == 16:
             v = values(rows)
             return v, np.abs(v)
-        by = rows.copy().view(np.uint8).reshape(self.H, n, -1)
-        codes = by if self.bits == 8 else np.stack((by & 15, by >> 4), -1).reshape(self.H, n, -1)
+        by = rows.copy().view(np.uint8).reshape(self.H, n, self.D * self.bits // 8)
+        codes = by if self.bits == 8 else np.stack((by & 15, by >> 4), -1).reshape(self.H, n, self.D)
         sv = np.repeat(values(s[pages, :, at].transpose(1, 0, 2)), self.gs, -1)
         bv = np.repeat(values(bias[pages, :, at].transpose(1, 0, 2)), self.gs, -1)
         return sv * codes + bv, np.abs(sv) * codes + (np.abs(bv) if name == "k" else 0.0)
