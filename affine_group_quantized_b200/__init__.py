@@ -263,9 +263,8 @@ def affine_dequantize(w_q, scales, biases, w_hat, N, K, bits, group_size,
 # ---------------------------------------------------------------------------
 
 
-def _check_kv(func: str, rc: int):
-    if rc != QMV_OK:
-        raise QmvError(func, rc, lib().qmv_kv_last_error().decode())
+def _kv_error(func: str, rc: int):
+    raise QmvError(func, rc, _kv().last_error())
 
 
 class KVCache:
@@ -336,7 +335,7 @@ def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, t
         cache._address, cache._device, k, v, block_table, lens, token_starts, batch, num_tokens,
         table_width, seen, positions, weights, state_width, k_stride, v_stride, d_status, stream)
     if rc:
-        _check_kv("kv_append", rc)
+        _kv_error("kv_append", rc)
 
 
 def kv_read(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,
@@ -347,15 +346,16 @@ def kv_read(cache, k, v, block_table, lens, token_starts, batch, num_tokens, tab
         cache._address, cache._device, k, v, block_table, lens, token_starts, batch, num_tokens,
         table_width, k_stride, v_stride, d_status, stream)
     if rc:
-        _check_kv("kv_read", rc)
+        _kv_error("kv_read", rc)
 
 
 def kv_attention_workspace(cache, batch, num_q_heads, table_width, with_weights=False) -> int:
     """Bytes of workspace kv_attention needs for these sizes, whatever the lengths."""
     n = ctypes.c_size_t(0)
-    _check_kv("kv_attention_workspace", lib().kv_attention_workspace(
-        ctypes.byref(cache._struct), batch, num_q_heads, table_width, 1 if with_weights else 0,
-        ctypes.byref(n)))
+    rc = lib().kv_attention_workspace(ctypes.byref(cache._struct), batch, num_q_heads, table_width,
+                                      1 if with_weights else 0, ctypes.byref(n))
+    if rc:
+        raise QmvError("kv_attention_workspace", rc, lib().qmv_kv_last_error().decode())
     return n.value
 
 
@@ -369,7 +369,7 @@ def kv_attention(cache, q, block_table, lens, out, batch, num_q_heads, table_wid
         cache._address, cache._device, q, block_table, lens, out, batch, num_q_heads,
         table_width, scale, workspace, weights, state_width, q_stride, d_status, stream)
     if rc:
-        _check_kv("kv_attention", rc)
+        _kv_error("kv_attention", rc)
 
 
 def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_weights,
@@ -383,4 +383,4 @@ def kv_evict(cache, block_table, lens, seen, weights, positions, new_lens, new_w
         new_weights, new_positions, batch, table_width, state_width, budget, recent, sinks,
         d_status, stream)
     if rc:
-        _check_kv("kv_evict", rc)
+        _kv_error("kv_evict", rc)

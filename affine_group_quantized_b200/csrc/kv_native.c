@@ -340,6 +340,15 @@ static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
+/* last_error(): the message of the last non-OK status on this thread, from the
+ * library that this module calls */
+static PyObject *last_error(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  (void)a;
+  if (count_is(n, 0)) return NULL;
+  return PyUnicode_FromString(qmv_kv_last_error());
+}
+
 /* setup(current_device, current_stream) */
 static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
@@ -352,7 +361,7 @@ static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 #define FAST(name, f) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {FAST("append", append), FAST("read", read_),
                                 FAST("attention", attention), FAST("evict", evict),
-                                FAST("setup", setup), {NULL, NULL, 0, NULL}};
+                                FAST("last_error", last_error), FAST("setup", setup), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv_native", NULL, -1, methods, NULL, NULL,
                                     NULL, NULL};
 

@@ -38,8 +38,8 @@
  * Streams: `stream` is a cudaStream_t (NULL = the legacy default stream).
  * Every call only enqueues work on that stream and returns; results are
  * ready when the stream is synchronized.  Each successful call enqueues one
- * kernel (qmv's tensor-core path also enqueues a clear of new scratch, on
- * the same stream, when it allocates).
+ * kernel (kv_attention two; qmv's tensor-core path also enqueues a clear of
+ * new scratch, on the same stream, when it allocates).
  * Bounded waits: every wait inside the kernels gives up after a bound (a few
  * hundred milliseconds); a kernel whose wait gave up ORs 2 into a status
  * word -- gather_qmv's d_status when given, else the library's per-device
@@ -361,8 +361,10 @@ int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, lon
  *   workspace  device memory of kv_attention_workspace's bytes, 16-byte
  *            aligned; no contents are expected or kept.  Calls that may run at
  *            the same time need workspaces of their own.
- * Scores, softmax statistics and sums are fp32; a length past the sequence's
- * room is cut to it and flagged, and slots of a page outside the cache take
+ * Scores, softmax statistics and sums are fp32.  Each probability times a value
+ * scale is rounded once to fp16 (relative 2^-11; terms below 2^-33 of the largest
+ * scale met lose bits), each probability over bf16 rows once to bf16.  A length
+ * past the sequence's room is cut to it and flagged, and slots of a page outside the cache take
  * no part.  Results do not depend on timing (partial sums are joined in a
  * fixed order).  batch = 0 enqueues nothing.  No allocation.
  */
