@@ -1224,7 +1224,6 @@ attn_kernel(const AttnParams p) {
     }
     cp_wait<0>();
   }
-  let_next_grid_start();
   __syncthreads();  // the rings are free
   float4 *tails = reinterpret_cast<float4 *>(attn_smem);
   if (tail) write_piece<C>(sg, tails + warp * C::QUADS, piece_ml[1][warp], lane);
