@@ -10,7 +10,10 @@
 // them lie first (a thread each), and then goes through them with every thread
 // at a chunk of its own: its head and place in the head stay the same, so a
 // token costs it one row number.  A group of 32, 64 or 128 elements is 2, 4 or
-// 8 neighbouring lanes.
+// 8 neighbouring lanes.  Measured (B200, 8 heads of 128): 73.7 thousand 4-bit
+// tokens read in 71 us (5.4 TB/s, memory); 6655 tokens quantized to 8 bits in
+// about 17 us, bound by the quantizer's arithmetic (398 instructions for 16
+// elements of a lane).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -372,10 +375,13 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks<APPEND>()) kv_rows_ker
 // A (sequence, kv head)'s slots are shared out over the CTAs of a cluster.
 // The weights become keys in shared memory whose unsigned order is the order
 // of the choice, are read from memory once, and the key of the last kept slot
-// is found 8 bits at a time from a histogram added up over the cluster.  Then
+// is found 8 bits at a time from histograms added up over the cluster, the last few
+// candidates ranked at once.  Then
 // each CTA lists its evicted slots below the new length (holes) and its kept
 // ones at or above it (movers), in order, and the cluster's warps move the
-// i-th mover's rows into the i-th hole.
+// i-th mover's rows into the i-th hole.  Bound by that chain of steps, each of
+// which waits for the one before: one of 1025 slots in 128 rows takes 9.5 us,
+// 2048 of up to 16384 in 32 rows 27 us, 8 of them moving the rows at HBM rate.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMaxCluster = 8;

@@ -40,6 +40,12 @@
 // tiles ahead, and needs no barrier but its own until its range is done.  A
 // segment inside a warp's range is written out by it; pieces of a segment are
 // joined within the CTA, and those of CTAs by a second kernel, in order.
+//
+// Bound, and measured (B200): 4-bit rows by instruction issue (588 instructions
+// for a 32-slot tile of heads of 128: four sequences of 131072 slots, 604 MB, in
+// 126 to 132 us, 0.70 to 0.73 of the measured copy rate); 8-bit rows by memory (8 of
+// 32768, 571 MB, in 97 us, 0.90); calls of a few hundred slots by the look-ups,
+// one tile and the joins of two dependent kernels (10 us).
 #pragma once
 
 #include <cuda_bf16.h>
