@@ -205,7 +205,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float pow2(int e) {  // e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
-__device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 __device__ __forceinline__ __half2 as_half2(uint32_t v) {
   return *reinterpret_cast<const __half2 *>(&v);
 }
