@@ -326,7 +326,8 @@ typedef struct {
  *                new token of sequence b gets position seen[b] + i and
  *                accumulated weight 0
  * Quantized rows are bit-identical to affine_quantize's.  lens is read, not
- * advanced.  The pages written must not be shared by two tokens of the call.
+ * advanced.  No two tokens of a call may go to the same slot (a page named twice
+ * in the table): which of the two the row then holds is not defined.
  * num_tokens = 0 enqueues nothing.  One kernel; no allocation.
  */
 int kv_append(const qmv_kv_cache *cache, const void *k, const void *v, long long k_stride,
