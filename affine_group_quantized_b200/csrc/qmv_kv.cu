@@ -978,6 +978,29 @@ cudaError_t rows_launch(qmvc::RowParams &p, int sms, cudaStream_t st) {
                          : rows_g<APPEND, 16, 32>(p, sms, st);  // bf16 rows have no groups
 }
 
+// Arrays of 4-byte words in device memory: `rows` rows of `width` words, `pitch`
+// words apart.
+struct Words {
+  const char *name;
+  const void *at;
+  long long rows, width, pitch;
+};
+
+// Whether two of them have a word in common.  Rows i and j do where
+// -a.width < (a.at - b.at) + (i - j) * pitch < b.width; both have the pitch of
+// the state arrays, or one row.
+bool overlap(const Words &a, const Words &b) {
+  if (a.rows * a.width == 0 || b.rows * b.width == 0) return false;
+  const long long pitch = a.rows > 1 ? a.pitch : b.pitch;
+  const long long d = (static_cast<long long>(reinterpret_cast<uintptr_t>(b.at)) -
+                       static_cast<long long>(reinterpret_cast<uintptr_t>(a.at))) / 4;
+  // the first i - j above (d - a.width) / pitch that there is
+  const long long low = d - a.width;
+  long long t = low / pitch - (low % pitch < 0) + 1;
+  if (t < 1 - b.rows) t = 1 - b.rows;
+  return t < a.rows && t * pitch < d + b.width;
+}
+
 int check_state_width(const char *f, const qmvc::CacheView &c, int state_width) {
   if (state_width < c.width * c.S)
     return kfail(QMV_ERR_SHAPE, "%s: state_width=%d is below the sequence's room of %d slots", f,
@@ -1130,6 +1153,28 @@ int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens,
   const void *words[] = {lens, seen, weights, positions, new_lens, new_weights, new_positions};
   for (const void *w : words)
     if (!aligned(w, 4)) return kfail(QMV_ERR_ALIGN, "%s: state and length arrays must be 4-byte aligned", f);
+  // A cluster of one head may write new_lens, or its state, while those of other
+  // heads have yet to read their inputs.
+  const long long state_rows = static_cast<long long>(batch) * p.c.H;
+  const long long table_words = static_cast<long long>(batch) * table_width;
+  const Words read[] = {{"lens", lens, 1, batch, batch},
+                        {"seen", seen, 1, batch, batch},
+                        {"block_table", block_table, 1, table_words, table_words},
+                        {"weights", weights, state_rows, room, state_width},
+                        {"positions", positions, state_rows, room, state_width}};
+  const Words written[] = {{"new_lens", new_lens, 1, batch, batch},
+                           {"new_weights", new_weights, state_rows, room, state_width},
+                           {"new_positions", new_positions, state_rows, room, state_width}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      const bool in_place = i > 0 && j == i + 2 && written[i].at == read[j].at;
+      if (!in_place && overlap(written[i], read[j]))
+        return kfail(QMV_ERR_UNSUPPORTED, "%s: %s overlaps %s", f, written[i].name, read[j].name);
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i], written[j]))
+        return kfail(QMV_ERR_UNSUPPORTED, "%s: %s overlaps %s", f, written[i].name, written[j].name);
+  }
   if (batch == 0) return kok();
   Device dev;
   if ((rc = current_device(f, &dev))) return rc;

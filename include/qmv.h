@@ -398,6 +398,9 @@ int kv_attention_workspace(const qmv_kv_cache *cache, int batch, int num_q_heads
  *   new_weights, new_positions  as weights and positions, and possibly the
  *            same buffers: slots below new_lens[b] as they now are, slots from
  *            there to n cleared (0 and -1), slots from n on left as they were
+ * Otherwise no array that is written may have a word in common with another of
+ * the call's (new_lens not with lens or seen: heads that have not begun still
+ * read those); such calls return QMV_ERR_UNSUPPORTED.
  * A sequence's pages must be its own (no page in two rows of the table).
  * Slots of a page outside the cache move only their state.  A length past the
  * room is cut to it and flagged.  Room of at most 196608 slots.  batch = 0
