@@ -9,6 +9,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "qmv.h"
 
@@ -71,18 +72,24 @@ struct Device {
 };
 
 // Allows a kernel `bytes` of dynamic shared memory on a device, and once allowed
-// does not ask again (one `granted` per kernel; two threads may both ask).
+// does not ask again (one `granted` per kernel).  The attribute is the kernel's, not
+// the launch's, and calls of other sizes may ask at the same time: look, set and
+// note are one step, and the limit is only ever raised.
 struct Granted {
+  std::mutex mutex;
   std::atomic<int> bytes[kMaxDevices];
 };
 template <typename... KArgs>
 cudaError_t allow_smem(void (*kern)(KArgs...), Granted &granted, const Device &dev, int bytes) {
-  if (bytes <= granted.bytes[dev.id].load(std::memory_order_relaxed)) return cudaSuccess;
+  std::atomic<int> &allowed = granted.bytes[dev.id];
+  if (bytes <= allowed.load(std::memory_order_acquire)) return cudaSuccess;
+  std::lock_guard<std::mutex> hold(granted.mutex);
+  if (bytes <= allowed.load(std::memory_order_relaxed)) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)  // as many blocks of an SM as the rest allows
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess) granted.bytes[dev.id].store(bytes, std::memory_order_relaxed);
+  if (e == cudaSuccess) allowed.store(bytes, std::memory_order_release);
   else cudaGetLastError();  // clear it
   return e;
 }
