@@ -120,7 +120,9 @@ struct AttnCfg {
   static_assert(STAGES >= 2, "a tile is fetched while another is computed");
   static constexpr int TAIL = HEADS * D * 4;           // a warp's last piece
   static constexpr int SMEM = WARPS * (STAGES * STAGE > TAIL ? STAGES * STAGE : TAIL);
-  static_assert(SMEM + 4 * 4097 + 6144 <= 232448, "rings, the tiles' sums of 4096 sequences, and the rest");
+  // attn_kernel's arrays of fixed size, and up to 128 bytes to align the rings
+  static constexpr int FIXED = 40 * WARPS * HEADS + 8 * WARPS + 128 + 128;
+  static_assert(SMEM + 4 * 4097 + FIXED <= 232448, "rings, the tiles' sums of 4096 sequences, and the rest");
   static constexpr int MT = D / 16;                    // 16-element accumulator tiles
   static constexpr int QUADS = HEADS * D / 4;          // float4 of a piece
   // elements that one set of value words covers
@@ -1084,6 +1086,7 @@ __device__ __forceinline__ void add_quad(float4 &o, float2 a, const float4 &x) {
 template <class C>
 __device__ __forceinline__ Known sum_tiles(const AttnParams &p, int *cum, int threads) {
   __shared__ int part[32];
+  static_assert(sizeof(part) == 128, "counted by AttnCfg::FIXED");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + threads - 1) / threads;
   const int b0 = tid * per < p.batch ? tid * per : p.batch;
@@ -1152,6 +1155,8 @@ attn_kernel(const AttnParams p) {
   __shared__ int piece_seg[2][C::WARPS];              // segment, or -1
   __shared__ __align__(8) float factor[2 * C::WARPS][C::HEADS];
   __shared__ float2 joined[2 * C::WARPS][C::HEADS];   // maximum and sum of a piece's segment here
+  static_assert(sizeof(piece_ml) + sizeof(piece_seg) + sizeof(factor) + sizeof(joined) + 128 + 128 == C::FIXED,
+                "what the shared memory's limit is checked with");
   int *cum = reinterpret_cast<int *>(attn_smem + C::SMEM);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_previous_grid();
