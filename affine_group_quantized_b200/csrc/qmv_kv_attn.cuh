@@ -88,6 +88,13 @@ struct AttnParams {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazy = 3.0f;  // p <= 2^kLazy
 
+// A score in units of log2.  It is rounded before the maximum is subtracted, here as
+// in the maximum itself and in the stored scores: their differences are then exact
+// multiples of its last step.  (A fused multiply-add would subtract the maximum's
+// rounding from a score without it, which at scores of 2^30 is 2^6 of an exponent,
+// and at 2^9 3e-5 of a weight.)
+__device__ __forceinline__ float scaled(float s, float f) { return __fmul_rn(s, f); }
+
 template <int BITS_, int D_, int GS_, int NB_>
 struct AttnCfg {
   static constexpr int BITS = BITS_, D = D_, GS = BITS_ == 16 ? D_ : GS_, NB = NB_;
@@ -638,7 +645,7 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
           for (int blk = 0; blk < C::TB; ++blk)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-              if (16 * blk + 8 * half < have) at[16 * blk + 8 * half] = s[blk][nb][i + 2 * half] * sg.f[nb][i];
+              if (16 * blk + 8 * half < have) at[16 * blk + 8 * half] = scaled(s[blk][nb][i + 2 * half], sg.f[nb][i]);
         }
   }
 
@@ -695,10 +702,13 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
         float x = top[nb][i];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        const float m = fmaxf(sg.m[nb][i], x * sg.f[nb][i]);
+        const float m = fmaxf(sg.m[nb][i], scaled(x, sg.f[nb][i]));
         const float a = m == kNegInf ? 1.0f : ex2(sg.m[nb][i] - m);
         sg.m[nb][i] = m;
-        sg.allow[nb][i] = m == kNegInf ? kNegInf : (m + kLazy) / sg.f[nb][i];
+        // below the quotient by more than its roundings and the product's: a score
+        // that is allowed is m + kLazy at most, whatever the steps at m are
+        const float up = (m + kLazy) / sg.f[nb][i];
+        sg.allow[nb][i] = m == kNegInf ? kNegInf : fmaf(fabsf(up), -0x1p-21f, up);
         sg.l[nb][i] *= a;
 #pragma unroll
         for (int gr = 0; gr < C::G; ++gr) sg.pb[gr][nb][i] *= a;
@@ -720,7 +730,7 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
       for (int blk = 0; blk < C::TB; ++blk)
 #pragma unroll
         for (int j = i; j < 4; j += 2) {
-          s[blk][nb][j] = ex2(fmaf(s[blk][nb][j], sg.f[nb][i], -m));
+          s[blk][nb][j] = ex2(__fsub_rn(scaled(s[blk][nb][j], sg.f[nb][i]), m));
           sg.l[nb][i] += s[blk][nb][j];
         }
     }
