@@ -1341,8 +1341,8 @@ __device__ __forceinline__ float2 joined_stats(const AttnParams &p, int2 at, int
   float m = kNegInf, l = 0.0f;
   for (int c = at.x; c <= at.y; ++c) {
     const float2 ml = p.part_ml[(static_cast<long long>(c) * 2 + (c == at.x)) * C::HEADS + h];
-    const float up = fmaxf(m, ml.x);
-    if (up != kNegInf) l = l * ex2(m - up) + ex2(ml.x - up) * ml.y;
+    const float up = fmaxf(m, ml.x), us = up == kNegInf ? 0.0f : up;
+    l = l * ex2(m - us) + ex2(ml.x - us) * ml.y;  // (NaN stays)
     m = up;
   }
   return make_float2(m, l);
@@ -1453,7 +1453,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     __syncthreads();
     for (int r = 0; r < count; ++r) {
       const float m = all[r].x, inv = 1.0f / all[r].y;
-      if (m == kNegInf) continue;  // no slot of the row takes part
+      if (all[r].y == 0.0f) continue;  // no slot of the row takes part
       const float *s = p.scores + (static_cast<long long>(b) * p.Hq + hk * p.R + r0 + r) * p.room;
 #pragma unroll
       for (int i = 0; i < kWeightSlots / kJoinThreads; ++i) {

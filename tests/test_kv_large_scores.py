@@ -7,7 +7,7 @@ import torch
 
 from affine_group_quantized_b200 import synth
 from tests._kv import HostCache, attention, values
-from tests._parity import bf16_values, dev_bf16, host_bits
+from tests._parity import bf16_values, host_bits
 from tests.test_kv_attention import run
 
 pytestmark = pytest.mark.gpu
