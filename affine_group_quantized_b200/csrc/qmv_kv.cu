@@ -26,9 +26,12 @@
 #include <string>
 
 #include "qmv.h"
+#include "qmv_affine.cuh"
 #include "qmv_kv.h"
 
 namespace qmvc {
+
+using namespace qmva;
 
 namespace cg = cooperative_groups;
 
@@ -91,20 +94,6 @@ __device__ __forceinline__ uint32_t place_of(const RowParams &p, const int *star
   return cache_row(p.c, page, 0, slot - of * p.c.S);
 }
 
-// ---------------------------------------------------------------------------
-// The quantizer's binary32 steps, those of affine_quantize (qmv_quant.cu); the
-// rows of the two are tested to be the same bits
-// ---------------------------------------------------------------------------
-
-// Scale and bias of a group with range [lo, hi], hi >= 0.
-__device__ __forceinline__ float2 scale_bias(float lo, float hi, float n_bins) {
-  const float size = fmaxf(__fdiv_rn(__fsub_rn(hi, lo), n_bins), 1e-7f);
-  const bool low = fabsf(lo) > fabsf(hi);
-  const float edge = low ? lo : hi, step = low ? size : -size;
-  const float q0 = roundf(__fdiv_rn(edge, step));
-  return q0 == 0.0f ? make_float2(step, 0.0f) : make_float2(__fdiv_rn(edge, q0), edge);
-}
-
 // A chunk: 16 bf16 elements, or the words of 16 codes.
 struct Chunk {
   uint32_t w[8];
@@ -135,38 +124,9 @@ __device__ __forceinline__ void store32(void *to, const Chunk &x, bool wide) {
   }
 }
 
-// The codes of 8 elements, min(round((v - bias) / scale), n_bins) with halves
-// away from zero, as whole numbers.  The product with the rounded reciprocal is
-// within 3 * 2^-24 of the quotient, relative to it, so its nearest integer is
-// the code unless it lies within that of a half; elements within 2^-22 *
-// (n_bins + 1) of one take the IEEE division.  Adding and subtracting 1.5 * 2^23
-// rounds to the nearest integer (|t| < 2^22).
-template <int BITS>
-__device__ __forceinline__ void codes_of(float (&v)[8], float bias, float scale, float rcp) {
-  constexpr float n_bins = static_cast<float>((1 << BITS) - 1);
-  constexpr float kSure = 0.5f - (n_bins + 1.0f) * 0x1p-22f, kRound = 12582912.0f;
-  float r[8];
-  float most = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fmul_rn(__fsub_rn(v[i], bias), rcp);
-    r[i] = __fsub_rn(__fadd_rn(t, kRound), kRound);
-    most = fmaxf(most, fabsf(__fsub_rn(t, r[i])));
-  }
-  if (most > kSure) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = __fsub_rn(v[i], bias);
-      const float t = __fmul_rn(d, rcp);
-      if (fabsf(__fsub_rn(t, r[i])) > kSure) r[i] = roundf(__fdiv_rn(d, scale));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = fminf(r[i], n_bins);
-}
-
-// The range of a group, its chunks in GS / 16 neighbouring lanes: (largest, and
-// at least 0; smallest).  In pairs of bf16, whose comparisons are exact.
+// The range of a group, its chunks in GS / 16 neighbouring lanes: (largest, from 0
+// up; smallest, from kRangeStart down).  In pairs of bf16, whose comparisons are
+// exact and take the number beside a NaN.
 template <int GS>
 __device__ __forceinline__ float2 group_range(const Chunk &x) {
   auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
@@ -182,7 +142,7 @@ __device__ __forceinline__ float2 group_range(const Chunk &x) {
     hi = __hmax2(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   return make_float2(fmaxf(fmaxf(__low2float(hi), __high2float(hi)), 0.0f),
-                     fminf(__low2float(lo), __high2float(lo)));
+                     fminf(fminf(__low2float(lo), __high2float(lo)), kRangeStart));
 }
 
 // 16 bf16 elements to 16 codes (2 * BITS bytes), with the group's scale and bias.
@@ -327,7 +287,7 @@ __global__ void __launch_bounds__(kRowThreads, row_blocks<APPEND>()) kv_rows_ker
         if constexpr (APPEND && BITS != 16) {
           static_assert(kRowAhead == 2, "a lane for each chunk of a group's lanes");
           const float2 r0 = group_range<GS>(x[0]), r1 = group_range<GS>(x[1]);
-          const float2 sb = scale_bias(tid & 1 ? r1.y : r0.y, tid & 1 ? r1.x : r0.x,
+          const float2 sb = group_step_offset(tid & 1 ? r1.y : r0.y, tid & 1 ? r1.x : r0.x,
                                        static_cast<float>((1 << BITS) - 1));
           scale = sb.x;
           bias = sb.y;

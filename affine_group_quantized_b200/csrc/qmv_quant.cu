@@ -24,14 +24,13 @@
 #include <string>
 
 #include "qmv.h"
+#include "qmv_affine.cuh"
 
 namespace qmvq {
 
-constexpr int kThreads = 256;
+using namespace qmva;
 
-__device__ __forceinline__ float bf16_bits_to_float(uint32_t h) {
-  return __uint_as_float(h << 16);
-}
+constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------------------
 // Dequantize: out = bf16(scale * q + bias), the exact value rounded once
@@ -165,52 +164,6 @@ __device__ __forceinline__ void store_chunk(uint8_t *wq, long long c, uint64_t p
   }
 }
 
-// One lane per chunk; the GS / 8 lanes of a group are consecutive, and a
-// warp's 32 chunks start on a group boundary, so the group's min and max are
-// butterfly reductions inside those lanes.  All 32 lanes run every
-// iteration (the loop bound is uniform over the warp); lanes past the end
-// load nothing and store nothing, and since the chunk count is a whole number
-// of groups they never share a group with a live lane.
-// The code of one element: min(round(d / scale), n_bins) with the page's
-// binary32 quotient d / scale and round-half-away.  The quotient is formed
-// as d * (1 / scale) (both correctly rounded), within 3 * 2^-24 of the
-// binary32 quotient relative to it; where no half-integer lies within
-// 2^-20 * max(|t|, 1) of that product, both round to the same integer and
-// rint gives it.  Only the rare elements near a half-integer take the IEEE
-// division and roundf, so every code is the one the page's steps decide.
-__device__ __forceinline__ uint32_t quantize_code(float v, float bias, float scale, float rcp,
-                                                  float n_bins) {
-  const float d = __fsub_rn(v, bias);
-  const float tp = __fmul_rn(d, rcp);
-  const float rt = rintf(tp);
-  float code = rt;
-  if (fabsf(__fsub_rn(tp, rt)) > 0.5f - fmaxf(fabsf(tp), 1.0f) * 0x1p-20f)
-    code = roundf(__fdiv_rn(d, scale));
-  return static_cast<uint32_t>(fminf(code, n_bins));
-}
-
-// The affine map of one group from its range [lo, hi] (lo taken from the
-// largest finite bf16 down, hi from 0 up, as the page's affine_quantize
-// starts them), in binary32 with IEEE divisions:
-//   * the code step has magnitude max((hi - lo) / n_bins, 1e-7);
-//   * the anchor is the endpoint of larger magnitude (hi on a tie); the step
-//     takes the anchor's sign when the anchor is lo, the opposite sign when
-//     it is hi, so codes grow away from the anchor into the range;
-//   * the anchor's position on the code grid, j = round(anchor / step)
-//     (halves away from zero), refines the step to anchor / j, and the
-//     anchor becomes the offset -- unless j = 0, when the step stays and the
-//     offset is 0.
-// Returns the step (the stored scale) and the offset (the stored bias).
-__device__ __forceinline__ float2 group_step_offset(float lo, float hi, float n_bins) {
-  const float magnitude = fmaxf(__fdiv_rn(__fsub_rn(hi, lo), n_bins), 1e-7f);
-  const bool anchor_is_lo = fabsf(lo) > fabsf(hi);
-  const float anchor = anchor_is_lo ? lo : hi;
-  const float step = anchor_is_lo ? magnitude : -magnitude;
-  const float j = roundf(__fdiv_rn(anchor, step));
-  if (j == 0.0f) return make_float2(step, 0.0f);
-  return make_float2(__fdiv_rn(anchor, j), anchor);
-}
-
 // One work item: 32 chunks (one warp, lane = chunk).  Finds the group's
 // range with xor butterflies over the group's lanes, stores the group's
 // scale and bias from its first lane and the lane's packed codes.
@@ -221,7 +174,6 @@ __device__ __forceinline__ void quantize_item(const uint4 raw, long long c, bool
                                               uint16_t *__restrict__ biases) {
   constexpr int kLanes = GS / 8;  // lanes per group
   const float n_bins = static_cast<float>((1 << BITS) - 1);
-  const float start_lo = bf16_bits_to_float(0x7f7fu);  // largest finite bf16
   const uint32_t pr[4] = {raw.x, raw.y, raw.z, raw.w};
   float v[8];
 #pragma unroll
@@ -229,7 +181,7 @@ __device__ __forceinline__ void quantize_item(const uint4 raw, long long c, bool
     v[2 * i] = __uint_as_float(pr[i] << 16);
     v[2 * i + 1] = __uint_as_float(pr[i] & 0xffff0000u);
   }
-  float lo = start_lo, hi = 0.0f;
+  float lo = kRangeStart, hi = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     lo = fminf(lo, v[i]);

@@ -325,7 +325,8 @@ typedef struct {
  *                state_width], state_width >= table_width*page_size: the i-th
  *                new token of sequence b gets position seen[b] + i and
  *                accumulated weight 0
- * Quantized rows are bit-identical to affine_quantize's.  lens is read, not
+ * Quantized rows are bit-identical to affine_quantize's (NaN and infinities too,
+ * which neither gives a meaning).  lens is read, not
  * advanced.  No two tokens of a call may go to the same slot (a page named twice
  * in the table): which of the two the row then holds is not defined.
  * num_tokens = 0 enqueues nothing.  One kernel; no allocation.
