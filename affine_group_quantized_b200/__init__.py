@@ -10,7 +10,8 @@ Arguments may be ``torch.Tensor`` (CUDA, contiguous; the data pointer is
 passed) or plain integer device addresses.  bf16 buffers are ``torch.bfloat16``
 tensors (or any 2-byte dtype holding bf16 bit patterns), packed weights are
 ``torch.int32``/``torch.uint32`` tensors.  ``stream`` defaults to the current
-torch CUDA stream.
+torch CUDA stream.  The ``kv_*`` calls refuse tensors of other types (float16 for
+bf16, int64 or float32 for int32, ...); the others look at sizes alone.
 """
 from __future__ import annotations
 
@@ -280,10 +281,12 @@ class KVCache:
         rows = num_pages * num_kv_heads * page_size
         for name, t in (("k", k), ("v", v)):
             _need(name, t, rows * head_dim * bits // 8)
+            _of_type(name, t, bits == 16)
         if bits != 16:
             for name, t in (("k_scales", k_scales), ("k_biases", k_biases),
                             ("v_scales", v_scales), ("v_biases", v_biases)):
                 _need(name, t, 2 * rows * (head_dim // max(group_size, 1)))
+                _of_type(name, t, True)
         self.buffers = (k, v, k_scales, k_biases, v_scales, v_biases)
         self.num_pages, self.num_kv_heads, self.page_size = num_pages, num_kv_heads, page_size
         self.head_dim, self.bits, self.group_size = head_dim, bits, group_size
@@ -291,6 +294,22 @@ class KVCache:
                                       page_size, head_dim, bits, group_size)
         self._address = ctypes.addressof(self._struct)
         self._device = _device_of(k)
+
+
+def _bf16_types():
+    """bf16, and the 2-byte integers that hold its bit patterns."""
+    import torch
+    return (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _of_type(name, t, bf16):
+    """A cache buffer holds bf16 values, or packed codes (any integers)."""
+    if t is None or isinstance(t, int):
+        return
+    if bf16 and t.dtype not in _bf16_types():
+        raise ValueError(f"{name}: must hold bf16 values, not {t.dtype}")
+    if not bf16 and (t.dtype.is_floating_point or t.dtype.is_complex):
+        raise ValueError(f"{name}: must hold packed codes (integers), not {t.dtype}")
 
 
 def _device_of(t):
@@ -320,7 +339,8 @@ def _kv():
         _kv_native.setup(
             getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
             getattr(torch._C, "_cuda_getCurrentRawStream",
-                    lambda d: torch.cuda.current_stream(d).cuda_stream))
+                    lambda d: torch.cuda.current_stream(d).cuda_stream),
+            _bf16_types(), (torch.int32, torch.uint32), (torch.float32,))
         _native = _kv_native
     return _native
 

@@ -2,7 +2,7 @@
  * kv_native.c -- the kv_* calls of the Python binding, as a CPython module.
  *
  * A decode step makes several of these calls, of a few microseconds of GPU work
- * each: looking at some eight tensors per call (size, contiguity, element size,
+ * each: looking at some eight tensors per call (size, contiguity, type,
  * device, address) and converting seventeen arguments took the interpreter and
  * ctypes longer than the kernels.  Each function here takes what its Python
  * wrapper was given, checks it, and calls the C entry point of include/qmv.h;
@@ -14,11 +14,16 @@
 
 #include "qmv.h"
 
-static PyObject *s_nbytes, *s_is_contiguous, *s_element_size, *s_get_device, *s_data_ptr, *s_dim,
+static PyObject *s_nbytes, *s_is_contiguous, *s_dtype, *s_get_device, *s_data_ptr, *s_dim,
     *s_shape, *s_stride, *s_cuda_stream;
 
 /* torch's current-device and current-stream functions, handed over by setup() */
 static PyObject *f_current_device, *f_current_stream;
+
+/* What an argument holds, and the torch types that do (tuples, by setup()). */
+enum { ANY, BF16, INT, FLOAT, KINDS };
+static PyObject *types_of[KINDS];
+static const char *const holds[KINDS] = {"", "bf16 values", "4-byte integers", "4-byte floats"};
 
 static int as_ll(PyObject *o, long long *out) { /* steals o */
   if (!o) return -1;
@@ -39,6 +44,19 @@ static int on_device(PyObject *t, const char *name, long long device) {
     return -1;
   }
   return 0;
+}
+
+static int of_type(PyObject *t, const char *name, int kind) {
+  Py_ssize_t i, n;
+  PyObject *types = types_of[kind], *o;
+  if (!types) return 0;
+  if (!(o = PyObject_GetAttr(t, s_dtype))) return -1;
+  Py_DECREF(o); /* (torch keeps its types) */
+  n = PyTuple_GET_SIZE(types);
+  for (i = 0; i < n; ++i)
+    if (PyTuple_GET_ITEM(types, i) == o) return 0;
+  PyErr_Format(PyExc_ValueError, "%s: must hold %s", name, holds[kind]);
+  return -1;
 }
 
 static int plain(PyObject *t, void **out, int *done) {
@@ -63,9 +81,9 @@ static int address(PyObject *t, void **out) {
   return PyErr_Occurred() ? -1 : 0;
 }
 
-/* An argument of at least `need` bytes, contiguous, of `size`-byte elements
- * (0: any), on the cache's device. */
-static int arg(PyObject *t, const char *name, long long need, int size, long long device, void **out) {
+/* An argument of at least `need` bytes, contiguous, of the kind's types, on the
+ * cache's device. */
+static int arg(PyObject *t, const char *name, long long need, int kind, long long device, void **out) {
   int done, yes;
   long long n;
   PyObject *o;
@@ -82,14 +100,7 @@ static int arg(PyObject *t, const char *name, long long need, int size, long lon
     PyErr_Format(PyExc_ValueError, "%s: must be contiguous", name);
     return -1;
   }
-  if (size) {
-    if (call_ll(t, s_element_size, &n)) return -1;
-    if (n != size) {
-      PyErr_Format(PyExc_ValueError, "%s: must hold %d-byte values", name, size);
-      return -1;
-    }
-  }
-  if (on_device(t, name, device)) return -1;
+  if (of_type(t, name, kind) || on_device(t, name, device)) return -1;
   return address(t, out);
 }
 
@@ -132,11 +143,7 @@ static int arg_rows(PyObject *t, const char *name, PyObject *given, long long ro
     if (n == 3) {
       if (three(PyObject_GetAttr(t, s_shape), shape)) return -1;
       if (shape[0] == rows && shape[1] == heads && shape[2] == dim) {
-        if (call_ll(t, s_element_size, &n) || three(PyObject_CallMethodNoArgs(t, s_stride), st)) return -1;
-        if (n != 2) {
-          PyErr_Format(PyExc_ValueError, "%s: must hold bf16 values", name);
-          return -1;
-        }
+        if (of_type(t, name, BF16) || three(PyObject_CallMethodNoArgs(t, s_stride), st)) return -1;
         if ((dim > 1 && st[2] != 1) || (heads > 1 && st[1] != dim)) {
           PyErr_Format(PyExc_ValueError, "%s: a row's heads must be contiguous", name);
           return -1;
@@ -147,7 +154,7 @@ static int arg_rows(PyObject *t, const char *name, PyObject *given, long long ro
       }
     }
   }
-  return arg(t, name, rows > 0 ? 2 * ((rows - 1) * *stride + packed) : 0, 2, device, out);
+  return arg(t, name, rows > 0 ? 2 * ((rows - 1) * *stride + packed) : 0, BF16, device, out);
 }
 
 /* What every call begins with: the cache's struct, device and shape. */
@@ -236,13 +243,13 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   slots = 4LL * batch * H * state;
   if (arg_rows(a[2], "k", a[14], tokens, H, D, c.device, &k, &ks) ||
       arg_rows(a[3], "v", a[15], tokens, H, D, c.device, &v, &vs) ||
-      arg(a[4], "block_table", 4LL * batch * width, 4, c.device, &table) ||
-      arg(a[5], "lens", 4LL * batch, 4, c.device, &lens) ||
-      arg(a[6], "token_starts", 4LL * batch + 4, 4, c.device, &starts) ||
-      arg(a[10], "seen", 4LL * batch, 4, c.device, &seen) ||
-      arg(a[11], "positions", slots, 4, c.device, &positions) ||
-      arg(a[12], "weights", slots, 4, c.device, &weights) ||
-      arg(a[16], "d_status", 4, 4, c.device, &status) || stream_of(a[17], &c, &stream))
+      arg(a[4], "block_table", 4LL * batch * width, INT, c.device, &table) ||
+      arg(a[5], "lens", 4LL * batch, INT, c.device, &lens) ||
+      arg(a[6], "token_starts", 4LL * batch + 4, INT, c.device, &starts) ||
+      arg(a[10], "seen", 4LL * batch, INT, c.device, &seen) ||
+      arg(a[11], "positions", slots, INT, c.device, &positions) ||
+      arg(a[12], "weights", slots, FLOAT, c.device, &weights) ||
+      arg(a[16], "d_status", 4, INT, c.device, &status) || stream_of(a[17], &c, &stream))
     return NULL;
   rc = kv_append(c.cache, k, v, ks, vs, table, lens, starts, batch, tokens, width, seen, positions,
                  weights, state, status, stream);
@@ -264,10 +271,10 @@ static PyObject *read_(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   D = c.cache->head_dim;
   if (arg_rows(a[2], "k", a[10], tokens, H, D, c.device, &k, &ks) ||
       arg_rows(a[3], "v", a[11], tokens, H, D, c.device, &v, &vs) ||
-      arg(a[4], "block_table", 4LL * batch * width, 4, c.device, &table) ||
-      arg(a[5], "lens", 4LL * batch, 4, c.device, &lens) ||
-      arg(a[6], "token_starts", 4LL * batch + 4, 4, c.device, &starts) ||
-      arg(a[12], "d_status", 4, 4, c.device, &status) || stream_of(a[13], &c, &stream))
+      arg(a[4], "block_table", 4LL * batch * width, INT, c.device, &table) ||
+      arg(a[5], "lens", 4LL * batch, INT, c.device, &lens) ||
+      arg(a[6], "token_starts", 4LL * batch + 4, INT, c.device, &starts) ||
+      arg(a[12], "d_status", 4, INT, c.device, &status) || stream_of(a[13], &c, &stream))
     return NULL;
   rc = kv_read(c.cache, k, v, ks, vs, table, lens, starts, batch, tokens, width, status, stream);
   return PyLong_FromLong(rc);
@@ -296,13 +303,13 @@ static PyObject *attention(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   H = c.cache->num_kv_heads;
   D = c.cache->head_dim;
   if (arg_rows(a[2], "q", a[13], batch, heads, D, c.device, &q, &qs) ||
-      arg(a[3], "block_table", 4LL * batch * width, 4, c.device, &table) ||
-      arg(a[4], "lens", 4LL * batch, 4, c.device, &lens) ||
-      arg(a[5], "out", 2LL * batch * heads * D, 2, c.device, &out) ||
-      arg(a[10], "workspace", 0, 0, c.device, &workspace) ||
-      as_ll(PyObject_GetAttr(a[10], s_nbytes), &bytes) ||
-      arg(a[11], "weights", 4LL * batch * H * state, 4, c.device, &weights) ||
-      arg(a[14], "d_status", 4, 4, c.device, &status) || stream_of(a[15], &c, &stream))
+      arg(a[3], "block_table", 4LL * batch * width, INT, c.device, &table) ||
+      arg(a[4], "lens", 4LL * batch, INT, c.device, &lens) ||
+      arg(a[5], "out", 2LL * batch * heads * D, BF16, c.device, &out) ||
+      arg(a[11], "weights", 4LL * batch * H * state, FLOAT, c.device, &weights) ||
+      arg(a[14], "d_status", 4, INT, c.device, &status) ||
+      arg(a[10], "workspace", 0, ANY, c.device, &workspace) ||
+      as_ll(PyObject_GetAttr(a[10], s_nbytes), &bytes) || stream_of(a[15], &c, &stream))
     return NULL;
   rc = kv_attention(c.cache, q, qs, table, lens, out, batch, heads, width, (float)scale, weights, state,
                     workspace, (size_t)bytes, status, stream);
@@ -325,15 +332,15 @@ static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       as_int(a[15], "sinks", &sinks))
     return NULL;
   slots = 4LL * batch * c.cache->num_kv_heads * state;
-  if (arg(a[2], "block_table", 4LL * batch * width, 4, c.device, &table) ||
-      arg(a[3], "lens", 4LL * batch, 4, c.device, &lens) ||
-      arg(a[4], "seen", 4LL * batch, 4, c.device, &seen) ||
-      arg(a[5], "weights", slots, 4, c.device, &weights) ||
-      arg(a[6], "positions", slots, 4, c.device, &positions) ||
-      arg(a[7], "new_lens", 4LL * batch, 4, c.device, &new_lens) ||
-      arg(a[8], "new_weights", slots, 4, c.device, &new_weights) ||
-      arg(a[9], "new_positions", slots, 4, c.device, &new_positions) ||
-      arg(a[16], "d_status", 4, 4, c.device, &status) || stream_of(a[17], &c, &stream))
+  if (arg(a[2], "block_table", 4LL * batch * width, INT, c.device, &table) ||
+      arg(a[3], "lens", 4LL * batch, INT, c.device, &lens) ||
+      arg(a[4], "seen", 4LL * batch, INT, c.device, &seen) ||
+      arg(a[5], "weights", slots, FLOAT, c.device, &weights) ||
+      arg(a[6], "positions", slots, INT, c.device, &positions) ||
+      arg(a[7], "new_lens", 4LL * batch, INT, c.device, &new_lens) ||
+      arg(a[8], "new_weights", slots, FLOAT, c.device, &new_weights) ||
+      arg(a[9], "new_positions", slots, INT, c.device, &new_positions) ||
+      arg(a[16], "d_status", 4, INT, c.device, &status) || stream_of(a[17], &c, &stream))
     return NULL;
   rc = kv_evict(c.cache, table, lens, seen, weights, positions, new_lens, new_weights, new_positions,
                 batch, width, state, budget, recent, sinks, status, stream);
@@ -349,12 +356,19 @@ static PyObject *last_error(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return PyUnicode_FromString(qmv_kv_last_error());
 }
 
-/* setup(current_device, current_stream) */
+/* setup(current_device, current_stream, bf16 types, int types, float types) */
 static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  int k;
   (void)self;
-  if (count_is(n, 2)) return NULL;
+  if (count_is(n, 5)) return NULL;
+  for (k = BF16; k < KINDS; ++k)
+    if (!PyTuple_Check(a[1 + k])) {
+      PyErr_SetString(PyExc_TypeError, "tuples of types are wanted");
+      return NULL;
+    }
   Py_XSETREF(f_current_device, Py_NewRef(a[0]));
   Py_XSETREF(f_current_stream, Py_NewRef(a[1]));
+  for (k = BF16; k < KINDS; ++k) Py_XSETREF(types_of[k], Py_NewRef(a[1 + k]));
   Py_RETURN_NONE;
 }
 
@@ -370,7 +384,7 @@ PyMODINIT_FUNC PyInit__kv_native(void) {
     PyObject **to;
     const char *name;
   } names[] = {{&s_nbytes, "nbytes"},         {&s_is_contiguous, "is_contiguous"},
-               {&s_element_size, "element_size"}, {&s_get_device, "get_device"},
+               {&s_dtype, "dtype"},           {&s_get_device, "get_device"},
                {&s_data_ptr, "data_ptr"},     {&s_dim, "dim"},
                {&s_shape, "shape"},           {&s_stride, "stride"},
                {&s_cuda_stream, "cuda_stream"}};
