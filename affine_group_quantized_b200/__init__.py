@@ -293,7 +293,14 @@ class KVCache:
         self._struct = _KVCacheStruct(*(_ptr(t) for t in self.buffers), num_pages, num_kv_heads,
                                       page_size, head_dim, bits, group_size)
         self._address = ctypes.addressof(self._struct)
-        self._device = _device_of(k)
+        self._device = None
+        for name, t in zip(("k", "v", "k_scales", "k_biases", "v_scales", "v_biases"), self.buffers):
+            d = _device_of(t)
+            if self._device is None:
+                self._device = d
+            elif d not in (None, self._device):
+                raise ValueError(f"{name}: on device {d}, the buffers before it on device "
+                                 f"{self._device}")
 
 
 def _bf16_types():
@@ -335,14 +342,19 @@ def _kv():
             raise RuntimeError(
                 f"the binding's _kv_native module is missing ({e}): build it with "
                 "`python -m affine_group_quantized_b200.build`") from e
-        import torch
-        _kv_native.setup(
-            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
-            getattr(torch._C, "_cuda_getCurrentRawStream",
-                    lambda d: torch.cuda.current_stream(d).cuda_stream),
-            _bf16_types(), (torch.int32, torch.uint32), (torch.float32,))
+        _setup(_kv_native)
         _native = _kv_native
     return _native
+
+
+def _setup(native, current_device=None, current_stream=None):
+    """Hands the module torch's types and functions (or a test's)."""
+    import torch
+    native.setup(
+        current_device or getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+        current_stream or getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda d: torch.cuda.current_stream(d).cuda_stream),
+        _bf16_types(), (torch.int32, torch.uint32), (torch.float32,))
 
 
 def kv_append(cache, k, v, block_table, lens, token_starts, batch, num_tokens, table_width,

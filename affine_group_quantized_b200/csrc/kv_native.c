@@ -35,12 +35,18 @@ static int call_ll(PyObject *t, PyObject *method, long long *out) {
   return as_ll(PyObject_CallMethodNoArgs(t, method), out);
 }
 
+/* A tensor lies on the cache's device, which is the current one, or beside a cache
+ * of plain addresses (device -1) on the current one, where the launch goes. */
 static int on_device(PyObject *t, const char *name, long long device) {
   long long d;
-  if (device < 0) return 0;
   if (call_ll(t, s_get_device, &d)) return -1;
+  if (d < 0) {
+    PyErr_Format(PyExc_ValueError, "%s: not on a CUDA device", name);
+    return -1;
+  }
+  if (device < 0 && as_ll(PyObject_CallNoArgs(f_current_device), &device)) return -1;
   if (d != device) {
-    PyErr_Format(PyExc_ValueError, "%s: not on the cache's device %lld", name, device);
+    PyErr_Format(PyExc_ValueError, "%s: on device %lld, the call's device is %lld", name, d, device);
     return -1;
   }
   return 0;
