@@ -193,13 +193,9 @@ static int cache_of(PyObject *address_, PyObject *device, Cache *c) {
 static int stream_of(PyObject *s, const Cache *c, void **out) {
   PyObject *o = NULL;
   int rc = 0;
-  if (s == Py_None) {
-    PyObject *d;
-    if (c->device < 0) {
-      *out = NULL;
-      return 0;
-    }
-    if (!(d = PyLong_FromLongLong(c->device))) return -1;
+  if (s == Py_None) { /* the current one, of the cache's or else the current device */
+    PyObject *d = c->device < 0 ? PyObject_CallNoArgs(f_current_device) : PyLong_FromLongLong(c->device);
+    if (!d) return -1;
     o = PyObject_CallOneArg(f_current_stream, d);
     Py_DECREF(d);
   } else if (PyLong_Check(s)) {
