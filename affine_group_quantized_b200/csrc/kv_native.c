@@ -160,7 +160,13 @@ static int arg_rows(PyObject *t, const char *name, PyObject *given, long long ro
       }
     }
   }
-  return arg(t, name, rows > 0 ? 2 * ((rows - 1) * *stride + packed) : 0, BF16, device, out);
+  if (rows <= 0) return arg(t, name, 0, BF16, device, out);
+  if (__builtin_mul_overflow(rows - 1, *stride, &n) || __builtin_add_overflow(n, packed, &n) ||
+      __builtin_mul_overflow(n, 2, &n)) {
+    PyErr_Format(PyExc_ValueError, "%s: %lld rows %lld elements apart pass 64 bits", name, rows, *stride);
+    return -1;
+  }
+  return arg(t, name, n, BF16, device, out);
 }
 
 /* What every call begins with: the cache's struct, device and shape. */
