@@ -2,12 +2,13 @@
  * kv_native.c -- the kv_* calls of the Python binding, as a CPython module.
  *
  * A decode step makes several of these calls, of a few microseconds of GPU work
- * each: looking at some eight tensors per call (size, contiguity, type,
- * device, address) and converting seventeen arguments took the interpreter and
- * ctypes longer than the kernels.  Each function here takes what its Python
- * wrapper was given, checks it, and calls the C entry point of include/qmv.h;
- * it returns that call's status, or raises ValueError for an argument that it
- * refuses itself.  Arguments are tensors, plain integer addresses or None.
+ * each: looking at some eight tensors per call (size, contiguity, type, device,
+ * address) and converting seventeen arguments took the interpreter and ctypes
+ * longer than the kernels.  Each function here takes what its Python wrapper was
+ * given, checks it, and calls the C entry point of include/qmv.h; it returns that
+ * call's status, or raises ValueError for an argument that it refuses itself.
+ * Arguments are tensors, plain integer addresses or None.  Other Python threads run
+ * during the call, as with ctypes: a launch waits where its stream's queue is full.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -259,8 +260,10 @@ static PyObject *append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       arg(a[12], "weights", slots, FLOAT, c.device, &weights) ||
       arg(a[16], "d_status", 4, INT, c.device, &status) || stream_of(a[17], &c, &stream))
     return NULL;
+  Py_BEGIN_ALLOW_THREADS
   rc = kv_append(c.cache, k, v, ks, vs, table, lens, starts, batch, tokens, width, seen, positions,
                  weights, state, status, stream);
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
 
@@ -284,7 +287,9 @@ static PyObject *read_(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       arg(a[6], "token_starts", 4LL * batch + 4, INT, c.device, &starts) ||
       arg(a[12], "d_status", 4, INT, c.device, &status) || stream_of(a[13], &c, &stream))
     return NULL;
+  Py_BEGIN_ALLOW_THREADS
   rc = kv_read(c.cache, k, v, ks, vs, table, lens, starts, batch, tokens, width, status, stream);
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
 
@@ -319,8 +324,10 @@ static PyObject *attention(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       arg(a[10], "workspace", 0, ANY, c.device, &workspace) ||
       as_ll(PyObject_GetAttr(a[10], s_nbytes), &bytes) || stream_of(a[15], &c, &stream))
     return NULL;
+  Py_BEGIN_ALLOW_THREADS
   rc = kv_attention(c.cache, q, qs, table, lens, out, batch, heads, width, (float)scale, weights, state,
                     workspace, (size_t)bytes, status, stream);
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
 
@@ -350,8 +357,10 @@ static PyObject *evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       arg(a[9], "new_positions", slots, INT, c.device, &new_positions) ||
       arg(a[16], "d_status", 4, INT, c.device, &status) || stream_of(a[17], &c, &stream))
     return NULL;
+  Py_BEGIN_ALLOW_THREADS
   rc = kv_evict(c.cache, table, lens, seen, weights, positions, new_lens, new_weights, new_positions,
                 batch, width, state, budget, recent, sinks, status, stream);
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
 
