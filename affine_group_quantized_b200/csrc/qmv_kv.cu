@@ -18,12 +18,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
-#include <mutex>
-#include <string>
 
 #include "qmv.h"
 #include "qmv_affine.cuh"
@@ -763,21 +762,21 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictP
 
 namespace {
 
-thread_local std::string g_kv_error;
+// (an array, so that a refusal needs no memory and nothing is thrown through a C
+// entry point)
+thread_local char g_kv_error[512];
 
 int kfail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 int kfail(int code, const char *fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_kv_error, sizeof g_kv_error, fmt, ap);
   va_end(ap);
-  g_kv_error = buf;
   return code;
 }
 
 int kok() {
-  g_kv_error.clear();
+  g_kv_error[0] = 0;
   return QMV_OK;
 }
 
@@ -847,18 +846,20 @@ using qmvc::Device;
 
 // The current device and its SM count, asked once per device.
 int current_device(const char *f, Device *out) {
-  static int sms[qmvc::kMaxDevices];
-  static std::once_flag once[qmvc::kMaxDevices];
+  static std::atomic<int> known[qmvc::kMaxDevices];  // two threads may both ask
   int d = 0;
   const cudaError_t e = cudaGetDevice(&d);
   if (e != cudaSuccess || d < 0 || d >= qmvc::kMaxDevices)
     return kfail(QMV_ERR_CUDA, "%s: no usable CUDA device (%s)", f, cudaGetErrorString(e));
-  std::call_once(once[d], [&] {
-    if (cudaDeviceGetAttribute(&sms[d], cudaDevAttrMultiProcessorCount, d) != cudaSuccess) sms[d] = 0;
-  });
-  if (sms[d] <= 0) return kfail(QMV_ERR_CUDA, "%s: cannot query device %d", f, d);
+  int sms = known[d].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    const cudaError_t q = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d);
+    if (q != cudaSuccess || sms <= 0)
+      return kfail(QMV_ERR_CUDA, "%s: cannot query device %d (%s)", f, d, cudaGetErrorString(q));
+    known[d].store(sms, std::memory_order_relaxed);
+  }
   out->id = d;
-  out->sms = sms[d];
+  out->sms = sms;
   return QMV_OK;
 }
 
@@ -1169,6 +1170,6 @@ int kv_evict(const qmv_kv_cache *cache, const int *block_table, const int *lens,
                                              static_cast<cudaStream_t>(stream), p));
 }
 
-const char *qmv_kv_last_error(void) { return g_kv_error.c_str(); }
+const char *qmv_kv_last_error(void) { return g_kv_error; }
 
 }  // extern "C"
