@@ -24,8 +24,9 @@
 //     its query element or output makes up for), exactly.  Queries are scaled
 //     per head by a power of two that brings the largest to [2^14, 2^15), exact
 //     in fp16 for every bf16 within 2^24 of it.  p * scale is rounded once to
-//     fp16 (2^-11), after a power of two, common to a warp's slots, that brings
-//     the largest scale so far to about 2^9 (terms below 2^-33 of it lose bits).
+//     fp16, after a power of two, common to a warp's slots, that brings the largest
+//     scale so far to [2^9, 2^10): by 2^-11 of itself, or below fp16's normal range
+//     (2^-23 of that scale) by 2^-34 of the scale.
 //   bf16 rows are multiplied as they are, p rounded once to bf16 (2^-8).
 //   Sums are fp32 throughout.
 // The k index of a product may be any permutation of its 16 elements or slots

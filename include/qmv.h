@@ -364,11 +364,14 @@ int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, lon
  *            aligned; no contents are expected or kept.  Calls that may run at
  *            the same time need workspaces of their own.
  * Scores, softmax statistics and sums are fp32.  Each probability times a value
- * scale is rounded once to fp16 (relative 2^-11; terms below 2^-33 of the largest
- * scale met lose bits), each probability over bf16 rows once to bf16.  A length
- * past the sequence's room is cut to it and flagged, and slots of a page outside the cache take
- * no part.  Results do not depend on timing (partial sums are joined in a
- * fixed order).  batch = 0 enqueues nothing.  No allocation.
+ * scale is rounded once to fp16: by at most 2^-11 of itself, or, below 2^-23 of the
+ * largest value scale met before it, by at most 2^-34 of that scale.  Each
+ * probability over bf16 rows is rounded once to bf16.  |scale| and, over quantized
+ * rows, |scale| times a query's elements are to stay below 2^117.  out must not
+ * overlap the inputs.  A length past the sequence's room is cut to it and flagged,
+ * and slots of a page outside the cache take no part.  Results do not depend on
+ * timing (partial sums are joined in a fixed order).  batch = 0 enqueues nothing.
+ * No allocation.
  */
 int kv_attention(const qmv_kv_cache *cache, const void *q, long long q_stride,
                  const int *block_table, const int *lens, void *out, int batch, int num_q_heads,
