@@ -27,7 +27,11 @@
 //     fp16, after a power of two, common to a warp's slots, that brings the largest
 //     scale so far to [2^9, 2^10): by 2^-11 of itself, or below fp16's normal range
 //     (2^-23 of that scale) by 2^-34 of the scale.
-//   bf16 rows are multiplied as they are, p rounded once to bf16 (2^-8).
+//   bf16 rows are multiplied as they are, by p as the sum of two bf16 numbers, its
+//     rounding and that of the rest (2^-16): with the first alone p's rounding was
+//     as large as the output's.  The second product of a tile costs 0.5 % of a call
+//     (64 x 255 .. 2047 slots, 4 x 4 heads of 256: 66.4 -> 67.1 us), 3 % with 16
+//     heads to a kv head (16 x 512 .. 4096, 4 x 16 of 128: 20.1 -> 20.7).
 //   Sums are fp32 throughout.
 // The k index of a product may be any permutation of its 16 elements or slots
 // as long as both operands agree: it is chosen so that a 32-bit word of codes
@@ -741,12 +745,17 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
   for (int blk = 0; blk < C::TB; ++blk) {
     const uint32_t vb = vbase + blk * 16 * C::RB;
     if constexpr (BF) {
-      uint32_t b[C::NB][2];
+      uint32_t b[C::NB][2], rest[C::NB][2];
 #pragma unroll
-      for (int nb = 0; nb < C::NB; ++nb) {
-        b[nb][0] = movmatrix(pack16<true>(s[blk][nb][0], s[blk][nb][1]));
-        b[nb][1] = movmatrix(pack16<true>(s[blk][nb][2], s[blk][nb][3]));
-      }
+      for (int nb = 0; nb < C::NB; ++nb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float x0 = s[blk][nb][2 * half], x1 = s[blk][nb][2 * half + 1];
+          const uint32_t hi = pack16<true>(x0, x1);
+          b[nb][half] = movmatrix(hi);
+          rest[nb][half] = movmatrix(pack16<true>(x0 - __uint_as_float(hi << 16),
+                                                  x1 - __uint_as_float(hi & 0xffff0000u)));
+        }
       const int r = (lane & 7) + ((lane >> 4) << 3);
       const uint32_t a0 = vb + r * C::RB + ((((lane >> 3) & 1) ^ swizzle<C::CH>(lane & 7)) << 4);
 #pragma unroll
@@ -754,8 +763,10 @@ __device__ __forceinline__ void attend_tile(Segment<C> &sg, const AttnParams &p,
         uint32_t a[4];
         ldmatrix4<true>(a, chunk_at<C::CH>(a0, 2 * mt));
 #pragma unroll
-        for (int nb = 0; nb < C::NB; ++nb)
+        for (int nb = 0; nb < C::NB; ++nb) {
           mma<true>(sg.o[mt][nb], a[0], a[1], a[2], a[3], b[nb][0], b[nb][1]);
+          mma<true>(sg.o[mt][nb], a[0], a[1], a[2], a[3], rest[nb][0], rest[nb][1]);
+        }
       }
     } else {
       uint32_t bva[GW], bvb[GW];
