@@ -1024,6 +1024,10 @@ static int check_attention(const char *f, const qmv_kv_cache *cache, const int *
                  num_q_heads, c->H);
   if (num_q_heads > 65535)
     return kfail(QMV_ERR_UNSUPPORTED, "%s: num_q_heads=%d above 65535", f, num_q_heads);
+  // slots are numbered in 31 bits, the ends of tiles and of the weights' blocks behind
+  // the last one among them (check_cache leaves a room below 2^31)
+  if (width * c->S > 0x7fffffff - 4095)
+    return kfail(QMV_ERR_UNSUPPORTED, "%s: room of %d slots above 2^31 - 4096", f, width * c->S);
   // tiles of 16 slots and (for the weights) score rows are numbered in 31 bits
   if (static_cast<double>(batch) * num_q_heads * (static_cast<double>(width) * c->S / 16 + 1) >= 2147483648.0)
     return kfail(QMV_ERR_UNSUPPORTED, "%s: batch * num_q_heads * room above 2^35", f);

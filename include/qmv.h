@@ -368,7 +368,8 @@ int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, lon
  * largest value scale met before it, by at most 2^-34 of that scale.  Each
  * probability over bf16 rows enters as the sum of two bf16 numbers (off by at most
  * 2^-16 of itself).  |scale| and, over quantized rows, |scale| times a query's
- * elements are to stay below 2^117.  out must not overlap the inputs.  A length past the sequence's room is cut to it and flagged,
+ * elements are to stay below 2^117.  Room of at most 2^31 - 4096 slots.  out must not
+ * overlap the inputs.  A length past the sequence's room is cut to it and flagged,
  * and slots of a page outside the cache take no part.  Results do not depend on
  * timing (partial sums are joined in a fixed order).  batch = 0 enqueues nothing.
  * No allocation.
