@@ -294,7 +294,8 @@ class KVCache:
                                       page_size, head_dim, bits, group_size)
         self._address = ctypes.addressof(self._struct)
         self._device = None
-        for name, t in zip(("k", "v", "k_scales", "k_biases", "v_scales", "v_biases"), self.buffers):
+        names = ("k", "v", "k_scales", "k_biases", "v_scales", "v_biases")
+        for name, t in zip(names[:2 if bits == 16 else 6], self.buffers):
             d = _device_of(t)
             if self._device is None:
                 self._device = d

@@ -52,3 +52,10 @@ def test_tensors_beside_a_cache_of_tensors(said):
     said["device"] = 1
     with pytest.raises(ValueError, match="current device"):
         evict_call(cache)
+
+
+def test_scales_of_a_bf16_cache_are_ignored():
+    rows = [OnDevice(2 * 8 * 2 * 16 * 128, torch.bfloat16, 0) for _ in range(2)]
+    other = OnDevice(4, torch.float16, -1)
+    cache = agq.KVCache(*rows, other, other, other, other, 8, 2, 16, 128, 16, 0)
+    assert cache._device == 0
