@@ -416,9 +416,9 @@ class ClockSampler:
 # The sources the GEMV kernels and their launch plans are built from: the
 # recorded DRAM traffic is valid while these are unchanged.  (The producer
 # side of the format, qmv_quant.cu, has kernels of its own.)
-GEMV_SOURCES = ("qmv_api.cu", "qmv_decode.cuh", "qmv_device.cuh", "qmv_mma.cuh",
-                "qmv_qmm.cu", "qmv_qmm.h", "qmv_quant.cu", "qmv_qvm.cuh", "qmv_stream.cuh",
-                "qmv_trellis.cuh")
+GEMV_SOURCES = ("qmv_affine.cuh", "qmv_api.cu", "qmv_decode.cuh", "qmv_device.cuh",
+                "qmv_mma.cuh", "qmv_qmm.cu", "qmv_qmm.h", "qmv_quant.cu", "qmv_qvm.cuh",
+                "qmv_stream.cuh", "qmv_trellis.cuh")
 
 
 def source_hash():
