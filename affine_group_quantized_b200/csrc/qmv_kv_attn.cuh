@@ -50,11 +50,14 @@
 // segment inside a warp's range is written out by it; pieces of a segment are
 // joined within the CTA, and those of CTAs by a second kernel, in order.
 //
-// Bound, and measured (B200): 4-bit rows by instruction issue (588 instructions
-// for a 32-slot tile of heads of 128: four sequences of 131072 slots, 604 MB, in
-// 126 to 132 us, 0.70 to 0.73 of the measured copy rate); 8-bit rows by memory (8 of
-// 32768, 571 MB, in 97 us, 0.90); calls of a few hundred slots by the look-ups,
-// one tile and the joins of two dependent kernels (10 us).
+// Bound, and measured (B200): 4-bit rows by the latency of instructions that wait
+// for one another, at three warps a scheduler (some 590 for a 32-slot tile of heads of
+// 128; 0.60 issued a cycle, and in 0.40 of the cycles no warp ready; full issue would
+// take 0.56 of the time, the bytes 0.69: four sequences of 131072 slots, 604 MB, in
+// 123 to 139 us); 8-bit rows by memory (8 of 32768, 571 MB, in 97 us, 0.90 of the
+// measured copy rate); calls of a few hundred slots by the look-ups, one tile and
+// the joins of two dependent kernels (10 us).  With weights the scores go out and
+// come back to a second kernel, 7 of 28 us (8 x 1023 .. 8190 slots, 16 heads of 64).
 #pragma once
 
 #include <cuda_bf16.h>
