@@ -343,6 +343,7 @@ int kv_append(const qmv_kv_cache *cache, const void *k, const void *v, long long
  * rows token_starts[b] .. token_starts[b+1]-1 of k and v, each value
  * bf16(scale*q + bias) rounded once (affine_dequantize's), bf16 rows as they
  * are.  Rows that belong to no sequence are left as they were.
+ * k and v must not overlap.
  */
 int kv_read(const qmv_kv_cache *cache, void *k, void *v, long long k_stride, long long v_stride,
             const int *block_table, const int *lens, const int *token_starts, int batch,
