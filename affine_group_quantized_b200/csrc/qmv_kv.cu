@@ -11,7 +11,7 @@
 // at a chunk of its own: its head and place in the head stay the same, so a
 // token costs it one row number.  A group of 32, 64 or 128 elements is 2, 4 or
 // 8 neighbouring lanes.  Measured (B200, 8 heads of 128): 73.7 thousand 4-bit
-// tokens read in 71 us (5.4 TB/s, memory); 6655 tokens quantized to 8 bits, with
+// tokens read in 71 us (5.4 TB/s, memory); 6656 tokens quantized to 8 bits, with
 // state, in 16.8 us (6.4 us of bytes), by the barriers behind the tokens' look-ups
 // and state (2.4 warps wait there for each instruction issued) and by the
 // quantizer's arithmetic, whose 10.6 M instructions would issue in 9.3 us.
